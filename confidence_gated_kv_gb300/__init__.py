@@ -17,3 +17,4 @@ from .binding import (  # noqa: F401
     status_string,
     workspace_bytes,
 )
+from .prompt import Rotary, prompt_attention, prompt_status, qk_rotary  # noqa: F401

@@ -7,8 +7,10 @@ fails with an error: there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -18,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libconfkv.so")
 
 OK, EINVAL, ECAPACITY, ECUDA, ETIMEOUT, ENOTIMPL, EDEVICE, ESTATE = 0, -1, -2, -3, -4, -5, -6, -7
 Q_FP16, Q_BF16 = 0, 1
+FP16, BF16, FP32 = 0, 1, 2
 
 
 class ConfkvError(RuntimeError):
@@ -109,6 +112,15 @@ def lib() -> ctypes.CDLL:
             "confkv_block_offset": (i32, [i32, i32, i32, i32]),
             "confkv_confidence_noalloc": (ctypes.c_int, [vp, i32, i32, ctypes.c_double, ctypes.c_double,
                                                          ctypes.c_double, vp, vp]),
+            "confkv_prefill_begin": (ctypes.c_int, [vp, vp, vp]),
+            "confkv_prefill_layer": (ctypes.c_int, [vp, i32, vp, vp, i32, vp, vp, vp]),
+            "confkv_read_rows": (ctypes.c_int, [vp, ctypes.POINTER(i64)]),
+            "confkv_read_layer": (ctypes.c_int, [vp, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]),
+            "confkv_rotary_frequencies": (ctypes.c_int, [i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 +
+                                          [vp, ctypes.POINTER(ctypes.c_float)]),
+            "confkv_qk_rotary": (ctypes.c_int, [vp, vp]),
+            "confkv_prompt_attention": (ctypes.c_int, [vp, vp]),
+            "confkv_prompt_status": (ctypes.c_int, [ctypes.POINTER(i32), vp]),
             "confkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "confkv_version": (i32, []),
         }
@@ -148,6 +160,31 @@ def _ptr(t) -> Optional[int]:
     if t is None:
         return None
     return t.data_ptr()
+
+
+_dtype_codes = None
+
+
+def dtype_code(dtype) -> int:
+    """Code of a torch element type (CONFKV_FP16, CONFKV_BF16, CONFKV_FP32)."""
+    global _dtype_codes
+    if _dtype_codes is None:
+        import torch
+        _dtype_codes = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
+    code = _dtype_codes.get(dtype)
+    if code is None:
+        raise ValueError("element type %s is not supported" % dtype)
+    return code
+
+
+_same = contextlib.nullcontext()
+
+
+def on_device(dev):
+    """Context in which `dev` is the current device (launches go to the
+    current one); nothing to do when it already is."""
+    import torch
+    return _same if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 _raw_stream_fn = None
@@ -208,6 +245,9 @@ def launch_plan(cfg: Config, n8_bound: int, attn_ctas: int = 0):
     return int(sp.value), int(g.value), int(c.value)
 
 
+_PAIR = struct.Struct("=2q")
+
+
 class Cache:
     """A CONF-KV cache manager on the current CUDA device.
 
@@ -250,9 +290,77 @@ class Cache:
     def prefill(self, k, v, prefill_len: Sequence[int], stream=None):
         """k, v: device fp16 [L][B][Hkv][t_max][d]."""
         t_max = int(k.shape[3])
+        self._prompt_rows = None
         pl = (ctypes.c_int32 * self.B)(*[int(x) for x in prefill_len])
         _check(lib().confkv_prefill(self._h, pl, _ptr(k), _ptr(v), t_max, _stream(stream)),
                "confkv_prefill")
+
+    def prefill_begin(self, prefill_len: Sequence[int], stream=None):
+        """Start a prefill by layer: prompt length of every sequence (host
+        ints).  Write every layer with prefill_layer, then step."""
+        if len(prefill_len) != self.B:
+            raise ValueError("prefill_len: one length per sequence is wanted")
+        with on_device(self.device):
+            _check(lib().confkv_prefill_begin(self._h, struct.pack("=%di" % self.B, *prefill_len),
+                                              _stream(stream, self._dev_index)), "confkv_prefill_begin")
+        self._prompt_rows = sum(prefill_len)
+
+    def _packed(self, t, name, rows):
+        """Checks a packed [rows, Hkv, d] tensor of this cache's device."""
+        if t.dim() != 3 or tuple(t.shape[1:]) != (self.Hkv, self.d) or t.shape[0] != rows or t.stride(2) != 1:
+            raise ValueError("%s: [%d, %d, %d] with contiguous channels is wanted" % (name, rows, self.Hkv, self.d))
+        if t.device.type != "cuda" or t.device.index != self._dev_index:
+            raise ValueError("%s is on %s, not on the cache's device" % (name, t.device))
+
+    def prefill_layer(self, layer: int, k, v, stream=None):
+        """K/V of one layer for all sequences, [rows, Hkv, d] fp16 or bf16, the
+        sequences' rows one after another."""
+        rows = getattr(self, "_prompt_rows", None)
+        if rows is None:
+            raise ConfkvError(ESTATE, "prefill_layer before prefill_begin")
+        self._packed(k, "k", rows)
+        self._packed(v, "v", rows)
+        if k.dtype != v.dtype:
+            raise ValueError("k and v: one type is wanted")
+        with on_device(self.device):
+            _check(lib().confkv_prefill_layer(self._h, int(layer), k.data_ptr(), v.data_ptr(), dtype_code(k.dtype),
+                                              _PAIR.pack(*k.stride()[:2]), _PAIR.pack(*v.stride()[:2]),
+                                              _stream(stream, self._dev_index)), "confkv_prefill_layer")
+
+    def read_rows(self) -> int:
+        """Rows that always hold a layer's resident entries (exact until the
+        first step)."""
+        n = ctypes.c_int64()
+        _check(lib().confkv_read_rows(self._h, ctypes.byref(n)), "confkv_read_rows")
+        return int(n.value)
+
+    def read_layer(self, layer: int, dtype=None, out=None, stream=None) -> dict:
+        """Resident entries of one layer: dict of k, v [rows, Hkv, d]
+        (dequantised, fp16 by default or bf16), positions int32 [rows] and
+        cu_seqlens int32 [B + 1], new or those of `out`, whose k sets the rows
+        and type.  Sequence b has rows cu_seqlens[b] to cu_seqlens[b + 1]."""
+        import torch
+        if out is None:
+            n, dev, dt = self.read_rows(), self.device, torch.float16 if dtype is None else dtype
+            out = dict(k=torch.empty((n, self.Hkv, self.d), dtype=dt, device=dev),
+                       v=torch.empty((n, self.Hkv, self.d), dtype=dt, device=dev),
+                       positions=torch.empty(n, dtype=torch.int32, device=dev),
+                       cu_seqlens=torch.empty(self.B + 1, dtype=torch.int32, device=dev))
+        k, v, pos, cu = out["k"], out["v"], out["positions"], out["cu_seqlens"]
+        rows = k.shape[0]
+        self._packed(k, "k", rows)
+        self._packed(v, "v", rows)
+        if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
+            raise ValueError("k and v: one type is wanted")
+        for name, t, n in (("positions", pos, rows), ("cu_seqlens", cu, self.B + 1)):
+            if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != k.device:
+                raise ValueError("%s: a contiguous int32 vector of %d on the cache's device is wanted" % (name, n))
+        with on_device(self.device):
+            _check(lib().confkv_read_layer(self._h, int(layer), dtype_code(k.dtype), k.data_ptr(), v.data_ptr(),
+                                           _PAIR.pack(*k.stride()[:2]), _PAIR.pack(*v.stride()[:2]), pos.data_ptr(),
+                                           cu.data_ptr(), rows, _stream(stream, self._dev_index)),
+                   "confkv_read_layer")
+        return out
 
     def new_outputs(self):
         import torch

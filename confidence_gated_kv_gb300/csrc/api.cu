@@ -151,6 +151,7 @@ size_t layout(const Shape& s, char* base, Dev* d, Staging* st) {
   dd.queue = cv.take<uint32_t>(1);
   dd.arrive = cv.take<uint32_t>(lbs);
   dd.conf_ready = cv.take<uint32_t>(s.B);
+  dd.row0 = cv.take<long long>(s.B);
   // the persistent attention kernel takes its units longest first from a
   // queue over prestep's sorted order (round robin when there are too many
   // groups to sort in one prestep launch)
@@ -183,6 +184,9 @@ struct confkv_ctx {
   size_t ws_bytes = 0;
   int device = 0;
   bool prefilled = false;
+  std::vector<char> layer_open;             // layer-wise prefill: layers not yet written
+  int layers_open = 0;                      // their number (0: none in progress)
+  bool set_outside = false;                 // entries or clock set by import_unit / set_clock
   std::vector<int32_t> T0;
   long long steps = 0;
   long long n_bound = 0;    // max resident entries of any (l, b), new token excluded
@@ -312,11 +316,116 @@ int confkv_prefill(confkv_ctx* ctx, const int32_t* prefill_len, const void* k, c
   // the host copy of T0 is pageable: make sure it has been consumed
   if (cudaStreamSynchronize(st) != cudaSuccess) return CONFKV_ECUDA;
   ctx->prefilled = true;
+  ctx->layers_open = 0;
+  ctx->set_outside = false;
   ctx->steps = 0;
   ctx->pin_left = 0;
   ctx->n_bound = tmax0;
   ctx->n8_bound = std::max<long long>(0, tmax0 - s.W);
   return CONFKV_OK;
+}
+
+// CONFKV_ESTATE while `st` is being captured, for calls that change host state.
+static int refuse_capture(cudaStream_t st) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) return CONFKV_ECUDA;
+  return cs == cudaStreamCaptureStatusNone ? CONFKV_OK : CONFKV_ESTATE;
+}
+
+int confkv_prefill_begin(confkv_ctx* ctx, const int32_t* prefill_len, void* stream) {
+  if (!ctx || !prefill_len) return CONFKV_EINVAL;
+  const Shape& s = ctx->s;
+  long long longest = 0, rows = 0;
+  for (int b = 0; b < s.B; ++b) {
+    if (prefill_len[b] < 0) return CONFKV_EINVAL;
+    longest = std::max<long long>(longest, prefill_len[b]);
+    rows += prefill_len[b];
+  }
+  if (longest - s.W > s.cap) return CONFKV_ECAPACITY;
+  if (rows >= (1LL << 31) - 1) return CONFKV_ECAPACITY;
+  cudaStream_t st = as_stream(stream);
+  const int r = refuse_capture(st);
+  if (r != CONFKV_OK) return r;
+  ctx->prefilled = false;
+  ctx->set_outside = false;
+  ctx->layer_open.assign(s.L, 1);
+  ctx->layers_open = s.L;
+  ctx->T0.assign(prefill_len, prefill_len + s.B);
+  ctx->steps = 0;
+  ctx->pin_left = 0;
+  ctx->n_bound = longest;
+  ctx->n8_bound = std::max<long long>(0, longest - s.W);
+  return launch_prefill_reset(s, ctx->d, ctx->T0.data(), st) == 0 ? CONFKV_OK : CONFKV_ECUDA;
+}
+
+// Packed rows [row][KV head][d]: 16-byte vectors, rows that do not overlap.
+static bool packed_rows_ok(const void* p, const int64_t* stride, const Shape& s, long long rows) {
+  if (!p || !aligned(p, 16)) return false;
+  if (rows > 1 && (stride[0] < s.D || stride[0] % 8)) return false;
+  if (s.Hkv > 1 && (stride[1] < s.D || stride[1] % 8)) return false;
+  return rows < 2 || s.Hkv < 2 || stride[0] >= (s.Hkv - 1) * stride[1] + s.D ||
+         stride[1] >= (rows - 1) * stride[0] + s.D;
+}
+
+int confkv_prefill_layer(confkv_ctx* ctx, int32_t layer, const void* k, const void* v, int32_t dtype,
+                         const int64_t* k_stride, const int64_t* v_stride, void* stream) {
+  if (!ctx || layer < 0 || layer >= ctx->s.L) return CONFKV_EINVAL;
+  if (dtype != CONFKV_FP16 && dtype != CONFKV_BF16) return CONFKV_EINVAL;
+  if (ctx->layers_open == 0) return CONFKV_ESTATE;
+  const Shape& s = ctx->s;
+  long long rows = 0;
+  for (int b = 0; b < s.B; ++b) rows += ctx->T0[b];
+  const int64_t none[2] = {0, 0};
+  if (rows > 0) {
+    if (!k_stride || !v_stride) return CONFKV_EINVAL;
+    if (!packed_rows_ok(k, k_stride, s, rows) || !packed_rows_ok(v, v_stride, s, rows)) return CONFKV_EINVAL;
+  }
+  cudaStream_t st = as_stream(stream);
+  const int r = refuse_capture(st);
+  if (r != CONFKV_OK) return r;
+  if (launch_write_layer(s, ctx->d, layer, dtype == CONFKV_BF16, k, v, rows > 0 ? k_stride : none,
+                         rows > 0 ? v_stride : none, (int)ctx->n_bound, st) != 0)
+    return CONFKV_ECUDA;
+  if (ctx->layer_open[layer]) {
+    ctx->layer_open[layer] = 0;
+    ctx->prefilled = --ctx->layers_open == 0;
+  }
+  return CONFKV_OK;
+}
+
+int confkv_read_rows(confkv_ctx* ctx, int64_t* rows) {
+  if (!ctx || !rows) return CONFKV_EINVAL;
+  if (!ctx->prefilled) return CONFKV_ESTATE;
+  // n_bound covers every (layer, sequence) now; the replays of a reservation
+  // may run ahead of the host's count, up to the loosest budget.  A sequence
+  // also holds no more entries than it has seen positions, unless its state
+  // or clock was set from outside.
+  const long long ahead = ctx->pin_left;
+  const long long most = std::min(ctx->n_bound + ahead, std::max(ctx->n_bound, ctx->maxN + 1LL));
+  long long n = 0;
+  for (int b = 0; b < ctx->s.B; ++b)
+    n += ctx->set_outside ? most : std::min(most, ctx->T0[b] + ctx->steps + ahead);
+  *rows = n;
+  return CONFKV_OK;
+}
+
+int confkv_read_layer(confkv_ctx* ctx, int32_t layer, int32_t dtype, void* k, void* v, const int64_t* k_stride,
+                      const int64_t* v_stride, int32_t* positions, int32_t* cu, int64_t rows, void* stream) {
+  if (!ctx || layer < 0 || layer >= ctx->s.L || rows < 0 || rows >= (1LL << 31)) return CONFKV_EINVAL;
+  if (dtype != CONFKV_FP16 && dtype != CONFKV_BF16) return CONFKV_EINVAL;
+  if (!ctx->prefilled) return CONFKV_ESTATE;
+  if (!cu || !aligned(cu, 4)) return CONFKV_EINVAL;
+  const Shape& s = ctx->s;
+  const int64_t none[2] = {0, 0};
+  if (rows > 0) {
+    if (!k_stride || !v_stride || !positions || !aligned(positions, 4)) return CONFKV_EINVAL;
+    if (!packed_rows_ok(k, k_stride, s, rows) || !packed_rows_ok(v, v_stride, s, rows)) return CONFKV_EINVAL;
+  }
+  const long long n8 = std::min<long long>(s.cap, ctx->n8_bound + ctx->pin_left);
+  return launch_read_layer(s, ctx->d, layer, dtype == CONFKV_BF16, k, v, rows > 0 ? k_stride : none,
+                           rows > 0 ? v_stride : none, positions, cu, (int)rows, n8, as_stream(stream)) == 0
+             ? CONFKV_OK
+             : CONFKV_ECUDA;
 }
 
 // Launch shape of the attention kernel for an INT8 bound.
@@ -782,6 +891,7 @@ int confkv_export_unit(confkv_ctx* ctx, int32_t b, int32_t l, confkv_unit_host* 
 int confkv_import_unit(confkv_ctx* ctx, int32_t b, int32_t l, const confkv_unit_host* in,
                        void* stream) {
   if (!ctx || !in || b < 0 || l < 0 || b >= ctx->s.B || l >= ctx->s.L) return CONFKV_EINVAL;
+  if (ctx->layers_open > 0) return CONFKV_ESTATE;
   const Shape& s = ctx->s;
   const int D = s.D, Hkv = s.Hkv;
   if (in->n8 < 0 || in->n8 > s.cap || in->nR < 0 || in->nR > s.WR) return CONFKV_EINVAL;
@@ -836,6 +946,7 @@ int confkv_import_unit(confkv_ctx* ctx, int32_t b, int32_t l, const confkv_unit_
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return CONFKV_ECUDA;
   ctx->prefilled = true;
+  ctx->set_outside = true;
   ctx->pin_left = 0;   // bounds may have grown: a pinned plan no longer holds
   ctx->n_bound = std::max<long long>(ctx->n_bound, (long long)in->n8 + in->nR);
   ctx->n8_bound = std::max<long long>(ctx->n8_bound, in->n8);
@@ -853,6 +964,8 @@ int confkv_set_clock(confkv_ctx* ctx, const int32_t* prefill_len, int64_t steps,
   if (!ctx || !prefill_len || steps < 0) return CONFKV_EINVAL;
   for (int b = 0; b < ctx->s.B; ++b)
     if (prefill_len[b] < 0) return CONFKV_EINVAL;
+  if (ctx->layers_open > 0) return CONFKV_ESTATE;
+  ctx->set_outside = true;
   ctx->T0.assign(prefill_len, prefill_len + ctx->s.B);
   ctx->steps = steps;
   cudaStream_t st = as_stream(stream);

@@ -148,6 +148,16 @@ struct Dev {
   uint32_t* queue;                 // next sorted position to hand out (kSchedQueue; zeroed by prestep)
   uint32_t* arrive;                // [l*b] fused steps: units of (l, b) done this step
   uint32_t* conf_ready;            // [b] fused steps: step index + 1 once c and the budgets of b are written
+  long long* row0;                 // [b] layer-wise prefill: first packed row of b
+};
+
+// Prompt lengths of up to kMax sequences, passed by value to the kernel that
+// opens a layer-wise prefill (no copy from host memory, so no synchronisation).
+struct LengthChunk {
+  static constexpr int kMax = 512;
+  int first, count;
+  long long row0;                  // packed row of sequence `first`
+  int32_t len[kMax];
 };
 
 enum : int { kSchedRoundRobin = 0, kSchedQueue = 1 };
@@ -278,6 +288,14 @@ int launch_attention(const Shape& s, const Dev& d, const void* q, float* out, in
 // Grid and cluster size of the attention launch for `splits` CTAs per unit
 // (the persistent kernel when 1, whose CTAs are not clustered).
 void attention_grid(const Shape& s, const Dev& d, int splits, int* grid, int* cluster);
+// Layer-wise prefill and read-back (layer_io.cu).  The reset clears the
+// counters and per-step words and uploads the prompt lengths.
+int launch_prefill_reset(const Shape& s, const Dev& d, const int32_t* len, cudaStream_t stream);
+int launch_write_layer(const Shape& s, const Dev& d, int layer, bool bf16, const void* k, const void* v,
+                       const int64_t* k_stride, const int64_t* v_stride, int max_len, cudaStream_t stream);
+int launch_read_layer(const Shape& s, const Dev& d, int layer, bool bf16, void* k, void* v,
+                      const int64_t* k_stride, const int64_t* v_stride, int32_t* positions, int32_t* cu, int rows,
+                      long long n8_bound, cudaStream_t stream);
 int launch_select(const Shape& s, const Dev& d, long long step, int32_t* evicted_pos,
                   int32_t* n_evicted, cudaStream_t stream);
 int attention_smem_bytes(const Shape& s, int splits, int max_tokens);

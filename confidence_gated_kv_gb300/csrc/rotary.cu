@@ -1,0 +1,354 @@
+// RMS norms of queries and keys per head and the rotary rotation, in one
+// pass.  A row is one head of one token:
+//
+//   y = x * rsqrt(mean(x^2) + eps) * weight          (or y = x without weight)
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t) * mscale
+//
+// for the rot / 2 pairs of the first rot channels, t = position * frequency;
+// a pair is channels (2i, 2i + 1) or (i, i + rot / 2).
+//
+// Angles.  The frequencies come as turns per position in 64-bit fixed point
+// (unit 2^-64), so that position * frequency modulo one turn is one 64-bit
+// integer product, exact for every 32-bit position: an fp32 angle at
+// position 10^6 is off by up to 0.03 rad, this one by the rounding of its
+// top 32 bits (2^-31 half turns).  sincospi then needs no range reduction.
+//
+// The pass reads and writes every element once and is bound by HBM; a thread
+// keeps the sines and cosines of its 16 channels over several heads of a
+// token.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cmath>
+
+#include "../../include/confkv.h"
+#include "confkv_internal.cuh"
+
+namespace confkv {
+namespace {
+
+struct RotArgs {
+  int n, Hq, Hkv, d, rot, interleaved;
+  int in_type, w_type, q_type, k_type;
+  float eps, mscale;
+  const void *q, *k;
+  void *qo, *ko;
+  long long q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t, ko_h;
+  const void *qw, *kw;
+  const int32_t* pos;
+  const uint64_t* turns;
+  int slots;                 // thread groups per token
+};
+
+__device__ __forceinline__ float load1(const void* p, long long i, int type) {
+  if (type == CONFKV_FP32) return static_cast<const float*>(p)[i];
+  if (type == CONFKV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store1(void* p, long long i, int type, float x) {
+  if (type == CONFKV_FP32)
+    static_cast<float*>(p)[i] = x;
+  else if (type == CONFKV_BF16)
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+  else
+    static_cast<__half*>(p)[i] = __float2half_rn(x);
+}
+
+// 8 consecutive elements from element offset i (a multiple of 8).
+__device__ __forceinline__ void load8(const void* p, long long i, int type, float* x) {
+  if (type == CONFKV_FP32) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = f[0], b = f[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    return;
+  }
+  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 f;
+    if (type == CONFKV_BF16)
+      f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+    else
+      f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    x[2 * j] = f.x;
+    x[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8(void* p, long long i, int type, const float* x) {
+  if (type == CONFKV_FP32) {
+    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    f[0] = make_float4(x[0], x[1], x[2], x[3]);
+    f[1] = make_float4(x[4], x[5], x[6], x[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (type == CONFKV_BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void angle(const RotArgs& a, int pos, int i, float* c, float* s) {
+  const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[i];      // modulo one turn
+  sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, s, c);   // 2^-31: half turns
+  *c *= a.mscale;
+  *s *= a.mscale;
+}
+
+// TPR threads per row, two 8-channel chunks each.  Groups of TPR threads
+// take heads slot, slot + slots, ... of their token.
+template <int TPR>
+__global__ void __launch_bounds__(256) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
+  const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(gid % TPR), heads = a.Hq + a.Hkv;
+  const long long group = gid / TPR;
+  const int token = (int)(group / a.slots), slot = (int)(group % a.slots);
+  const bool in = token < a.n;
+  // chunks of this thread and whether they are rotated
+  const int half = a.rot / 16;                 // chunks of one half of the rotated part
+  int c0 = 2 * t, c1 = 2 * t + 1;
+  if (!a.interleaved && t < half) {
+    c0 = t;
+    c1 = t + half;
+  }
+  const bool r0 = c0 < 2 * half, r1 = c1 < 2 * half;
+  float co[8], si[8];
+  if (in && r0) {
+    const int pos = a.pos[token];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) angle(a, pos, 8 * t + i, &co[i], &si[i]);
+  }
+  for (int base = 0; base < heads; base += a.slots) {      // the same count for every thread
+    const int head = base + slot;
+    const bool on = in && head < heads;
+    const bool is_q = head < a.Hq;
+    float x[16];
+    if (on) {
+      const void* src = is_q ? a.q : a.k;
+      const long long off = is_q ? token * a.q_t + head * a.q_h : token * a.k_t + (head - a.Hq) * a.k_h;
+      load8(src, off + 8 * c0, a.in_type, x);
+      load8(src, off + 8 * c1, a.in_type, x + 8);
+    }
+    const void* weight = is_q ? a.qw : a.kw;
+    if (a.qw || a.kw) {
+      float ss = 0.f;
+      if (on) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+      }
+#pragma unroll
+      for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (on && weight) {
+        const float f = rsqrtf(ss * (1.f / (16 * TPR)) + a.eps);
+        float g[16];
+        load8(weight, 8 * c0, a.w_type, g);
+        load8(weight, 8 * c1, a.w_type, g + 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * f * g[i];
+      }
+    }
+    if (!on) continue;
+    if (a.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < 4 ? r0 : r1) {
+          const float u = x[2 * i], v = x[2 * i + 1];
+          x[2 * i] = u * co[i] - v * si[i];
+          x[2 * i + 1] = v * co[i] + u * si[i];
+        }
+      }
+    } else if (r0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = x[i], v = x[8 + i];
+        x[i] = u * co[i] - v * si[i];
+        x[8 + i] = v * co[i] + u * si[i];
+      }
+    }
+    void* dst = is_q ? a.qo : a.ko;
+    const int type = is_q ? a.q_type : a.k_type;
+    const long long off = is_q ? token * a.qo_t + head * a.qo_h : token * a.ko_t + (head - a.Hq) * a.ko_h;
+    store8(dst, off + 8 * c0, type, x);
+    store8(dst, off + 8 * c1, type, x + 8);
+  }
+}
+
+// Any head size, alignment and rotated part: one warp per row, the row in
+// shared memory.
+constexpr int kMaxDim = 512;
+constexpr int kAnyWarps = 4;
+__global__ void __launch_bounds__(32 * kAnyWarps) rotary_any_kernel(const __grid_constant__ RotArgs a) {
+  __shared__ float s_row[kAnyWarps][kMaxDim];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.Hq + a.Hkv;
+  const long long row = (long long)blockIdx.x * kAnyWarps + warp;
+  if (row >= (long long)a.n * heads) return;
+  const int token = (int)(row / heads), head = (int)(row % heads);
+  const bool is_q = head < a.Hq;
+  const void* src = is_q ? a.q : a.k;
+  const long long off = is_q ? token * a.q_t + head * a.q_h : token * a.k_t + (head - a.Hq) * a.k_h;
+  float* x = s_row[warp];
+  float ss = 0.f;
+  for (int i = lane; i < a.d; i += 32) {
+    x[i] = load1(src, off + i, a.in_type);
+    ss = fmaf(x[i], x[i], ss);
+  }
+  const void* weight = is_q ? a.qw : a.kw;
+  if (weight) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float f = rsqrtf(ss / a.d + a.eps);
+    for (int i = lane; i < a.d; i += 32) x[i] = x[i] * f * load1(weight, i, a.w_type);
+  }
+  __syncwarp();
+  const int half = a.rot / 2;
+  if (half) {
+    const int pos = a.pos[token];
+    for (int i = lane; i < half; i += 32) {
+      float c, s;
+      angle(a, pos, i, &c, &s);
+      const int i0 = a.interleaved ? 2 * i : i, i1 = a.interleaved ? 2 * i + 1 : i + half;
+      const float u = x[i0], v = x[i1];
+      x[i0] = u * c - v * s;
+      x[i1] = v * c + u * s;
+    }
+    __syncwarp();
+  }
+  void* dst = is_q ? a.qo : a.ko;
+  const int type = is_q ? a.q_type : a.k_type;
+  const long long out = is_q ? token * a.qo_t + head * a.qo_h : token * a.ko_t + (head - a.Hq) * a.ko_h;
+  for (int i = lane; i < a.d; i += 32) store1(dst, out + i, type, x[i]);
+}
+
+int type_bytes(int type) { return type == CONFKV_FP32 ? 4 : type == CONFKV_FP16 || type == CONFKV_BF16 ? 2 : 0; }
+
+// Every row starts on a 16-byte boundary.
+bool aligned16(const void* p, const int64_t* stride, int bytes, long long n, long long heads) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (n < 2 || stride[0] * bytes % 16 == 0) &&
+         (heads < 2 || stride[1] * bytes % 16 == 0);
+}
+
+// No two rows of an output share an element.
+bool rows_apart(const int64_t* stride, int d, long long n, long long heads) {
+  const long long t = stride[0], h = stride[1];
+  if (n > 1 && t < d) return false;
+  if (heads > 1 && h < d) return false;
+  if (n > 1 && heads > 1) return t >= (heads - 1) * h + d || h >= (n - 1) * t + d;
+  return true;
+}
+
+// An output that starts where its input does has the same rows.
+bool same_place(const void* p, const int64_t* ps, const void* o, const int64_t* os, long long n, long long heads) {
+  return p == o && (n < 2 || ps[0] == os[0]) && (heads < 2 || ps[1] == os[1]);
+}
+
+template <int TPR>
+void launch_rows(const RotArgs& a, cudaStream_t st) {
+  const long long threads = (long long)a.n * a.slots * TPR;
+  rotary_rows_kernel<TPR><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
+}
+
+}  // namespace
+}  // namespace confkv
+
+using namespace confkv;
+
+extern "C" int confkv_rotary_frequencies(int32_t rot, double base, int32_t scaling, double factor,
+                                         double original_length, double beta_fast, double beta_slow,
+                                         uint64_t* turns, float* mscale) {
+  if (!turns || !mscale || rot < 0 || rot % 2 || !(base > 1.0) || !std::isfinite(base)) return CONFKV_EINVAL;
+  if (scaling < CONFKV_ROTARY_PLAIN || scaling > CONFKV_ROTARY_YARN) return CONFKV_EINVAL;
+  if (scaling != CONFKV_ROTARY_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return CONFKV_EINVAL;
+  if (scaling == CONFKV_ROTARY_NTK && rot == 2) return CONFKV_EINVAL;
+  if (scaling == CONFKV_ROTARY_YARN &&
+      (!(original_length > 0.0) || !std::isfinite(original_length) || !(beta_slow >= 0.0) ||
+       !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+    return CONFKV_EINVAL;
+  const double tau = 6.283185307179586476925286766559;
+  if (scaling == CONFKV_ROTARY_NTK && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scaling == CONFKV_ROTARY_LINEAR) f /= factor;
+    if (scaling == CONFKV_ROTARY_YARN) {
+      double keep = (original_length * f / tau - beta_slow) / (beta_fast - beta_slow);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    turns[i] = (uint64_t)std::ldexp(f / tau, 64);          // f <= 1: below 2^62
+  }
+  *mscale = scaling == CONFKV_ROTARY_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return CONFKV_OK;
+}
+
+extern "C" int confkv_qk_rotary(const confkv_rotary_args* p, void* stream) {
+  if (!p || p->n < 0 || p->Hq < 1 || p->Hkv < 0 || p->rot < 0 || p->rot % 2 || p->rot > p->d) return CONFKV_EINVAL;
+  if (p->d < 1) return CONFKV_EINVAL;
+  if (p->d > kMaxDim) return CONFKV_ENOTIMPL;
+  const int in = type_bytes(p->in_dtype), wb = type_bytes(p->w_dtype), qb = type_bytes(p->q_out_dtype),
+            kb = type_bytes(p->k_out_dtype);
+  if (!in || !wb || !qb || !kb) return CONFKV_EINVAL;
+  if (!std::isfinite(p->mscale) || ((p->q_weight || p->k_weight) && !(p->eps >= 0.f && std::isfinite(p->eps))))
+    return CONFKV_EINVAL;
+  if (p->n == 0) return CONFKV_OK;
+  const bool keys = p->Hkv > 0;
+  if (!p->q || !p->q_out || (keys && (!p->k || !p->k_out))) return CONFKV_EINVAL;
+  if (p->rot && (!p->positions || !p->turns)) return CONFKV_EINVAL;
+  auto at = [](const void* x, int a) { return reinterpret_cast<uintptr_t>(x) % a == 0; };
+  if (!at(p->q, in) || !at(p->q_out, qb) || !at(p->positions, 4) || !at(p->turns, 8) || !at(p->q_weight, wb) ||
+      (keys && (!at(p->k, in) || !at(p->k_out, kb) || !at(p->k_weight, wb))))
+    return CONFKV_EINVAL;
+  if (!rows_apart(p->q_out_stride, p->d, p->n, p->Hq)) return CONFKV_EINVAL;
+  if (keys && !rows_apart(p->k_out_stride, p->d, p->n, p->Hkv)) return CONFKV_EINVAL;
+  // an output over its input: the same elements in the same places
+  if (p->q == p->q_out &&
+      (p->in_dtype != p->q_out_dtype || !same_place(p->q, p->q_stride, p->q_out, p->q_out_stride, p->n, p->Hq)))
+    return CONFKV_EINVAL;
+  if (keys && p->k == p->k_out &&
+      (p->in_dtype != p->k_out_dtype || !same_place(p->k, p->k_stride, p->k_out, p->k_out_stride, p->n, p->Hkv)))
+    return CONFKV_EINVAL;
+  RotArgs a{};
+  a.n = p->n; a.Hq = p->Hq; a.Hkv = p->Hkv; a.d = p->d; a.rot = p->rot; a.interleaved = p->interleaved != 0;
+  a.in_type = p->in_dtype; a.w_type = p->w_dtype; a.q_type = p->q_out_dtype; a.k_type = p->k_out_dtype;
+  a.eps = p->eps; a.mscale = p->mscale;
+  a.q = p->q; a.k = p->k; a.qo = p->q_out; a.ko = p->k_out;
+  a.q_t = p->q_stride[0]; a.q_h = p->q_stride[1]; a.k_t = p->k_stride[0]; a.k_h = p->k_stride[1];
+  a.qo_t = p->q_out_stride[0]; a.qo_h = p->q_out_stride[1];
+  a.ko_t = p->k_out_stride[0]; a.ko_h = p->k_out_stride[1];
+  a.qw = p->q_weight; a.kw = keys ? p->k_weight : nullptr;
+  a.pos = p->positions; a.turns = p->turns;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const long long heads = (long long)p->Hq + p->Hkv;
+  // Vectors of 8 channels: head sizes of 4, 8 or 16 threads, halves of the
+  // rotated part in whole vectors, every row on a 16-byte boundary.
+  const bool rows = (p->d == 64 || p->d == 128 || p->d == 256) && p->rot % 16 == 0 &&
+                    aligned16(p->q, p->q_stride, in, p->n, p->Hq) &&
+                    aligned16(p->q_out, p->q_out_stride, qb, p->n, p->Hq) &&
+                    (!keys || (aligned16(p->k, p->k_stride, in, p->n, p->Hkv) &&
+                               aligned16(p->k_out, p->k_out_stride, kb, p->n, p->Hkv))) &&
+                    at(a.qw, 16) && at(a.kw, 16);
+  if (rows) {
+    const int tpr = p->d / 16;
+    // one head per thread group until the GPU is full, then up to eight
+    const long long full = 152LL * 2048;
+    long long per = (long long)p->n * heads * tpr / full;
+    per = per < 1 ? 1 : per > 8 ? 8 : per;
+    a.slots = (int)((heads + per - 1) / per);
+    if ((long long)p->n * a.slots * tpr / 256 + 1 >= (1LL << 31)) return CONFKV_EINVAL;
+    if (tpr == 4) launch_rows<4>(a, st);
+    else if (tpr == 8) launch_rows<8>(a, st);
+    else launch_rows<16>(a, st);
+  } else {
+    const long long blocks = ((long long)p->n * heads + kAnyWarps - 1) / kAnyWarps;
+    if (blocks >= (1LL << 31)) return CONFKV_EINVAL;
+    rotary_any_kernel<<<(unsigned)blocks, 32 * kAnyWarps, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? CONFKV_OK : CONFKV_ECUDA;
+}

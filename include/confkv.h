@@ -52,6 +52,12 @@ extern "C" {
 #define CONFKV_Q_FP16 0
 #define CONFKV_Q_BF16 1
 
+/* Element types of the calls that take a dtype (the first two are the query
+ * types above). */
+#define CONFKV_FP16 0
+#define CONFKV_BF16 1
+#define CONFKV_FP32 2
+
 /*
  * Configuration.  Defaults on the pages: w = (0.4, 0.3, 0.3) and tau = 0.7
  * ([gist-de] Konfidenzschätzung; [rainbus] 核心方法), alpha = 0.65
@@ -121,6 +127,53 @@ void confkv_destroy(confkv_ctx* ctx);
  */
 int confkv_prefill(confkv_ctx* ctx, const int32_t* prefill_len, const void* k, const void* v,
                    int64_t t_max, void* stream);
+
+/*
+ * Prefill by layer: the same cache as confkv_prefill, from what a model has
+ * in hand while it runs its prompt -- one layer's K/V of all sequences, rows
+ * packed without padding -- so that no layer's K/V has to be kept.
+ *   confkv_prefill_begin  resets the cache and fixes the prompt lengths
+ *       (HOST array of B).  Until every layer is written the context is not
+ *       prefilled: confkv_step, confkv_read_layer, confkv_import_unit and
+ *       confkv_set_clock return CONFKV_ESTATE.  CONFKV_ECAPACITY if a length
+ *       minus W exceeds cap.
+ *   confkv_prefill_layer  writes layer `layer`: k, v device [rows][Hkv][d],
+ *       rows = the sum of the lengths, sequence b's rows after those of
+ *       b - 1; dtype CONFKV_FP16 or CONFKV_BF16 (converted to fp16 first).
+ *       Scales, codes and window are those of confkv_prefill on the same
+ *       values.  Layers in any order; one written twice keeps the last.
+ *       CONFKV_ESTATE outside confkv_prefill_begin .. last layer.
+ * Strides are in elements, row first, then KV head; channels are contiguous;
+ * base addresses are multiples of 16 bytes and strides of 8 elements.  With
+ * rows = 0, k, v and the strides may be NULL.  Both calls are asynchronous on
+ * `stream` and refuse stream capture (CONFKV_ESTATE), like every call that
+ * changes the host's bounds.
+ */
+int confkv_prefill_begin(confkv_ctx* ctx, const int32_t* prefill_len, void* stream);
+int confkv_prefill_layer(confkv_ctx* ctx, int32_t layer, const void* k, const void* v, int32_t dtype,
+                         const int64_t* k_stride, const int64_t* v_stride, void* stream);
+
+/*
+ * The resident entries of one layer as packed K/V, dequantised on the device
+ * (confkv_export_unit gives codes and scales to the host): for attention of
+ * further prompt tokens over a cache, or for handing a sequence on.
+ *   k, v       device [rows][Hkv][d], dtype CONFKV_FP16 or CONFKV_BF16:
+ *              fp16 window entries converted, INT8 entries code * scale, each
+ *              rounded once
+ *   positions  device int32 [rows]: absolute position of each row
+ *   cu         device int32 [B + 1], written: sequence b has rows cu[b] ..
+ *              cu[b+1]-1, INT8 entries in slot order (by position until the
+ *              first eviction), then the window by position
+ *   rows       rows the buffers hold; confkv_read_rows gives a bound that
+ *              always suffices (exact until the first step).  Entries beyond
+ *              `rows` are dropped and set CONFKV_STATUS_CAPACITY; rows behind
+ *              the last sequence are not written.
+ * Strides as in confkv_prefill_layer.  Needs a prefilled context (else
+ * CONFKV_ESTATE); asynchronous on `stream`, may be captured.
+ */
+int confkv_read_rows(confkv_ctx* ctx, int64_t* rows);
+int confkv_read_layer(confkv_ctx* ctx, int32_t layer, int32_t dtype, void* k, void* v, const int64_t* k_stride,
+                      const int64_t* v_stride, int32_t* positions, int32_t* cu, int64_t rows, void* stream);
 
 /*
  * One decode step for all B sequences: the token at position
@@ -402,6 +455,105 @@ int32_t confkv_block_offset(int32_t kind, int32_t d, int32_t tau, int32_t c);
  */
 int confkv_confidence_noalloc(const float* logits, int32_t B, int32_t V, double w_H, double w_m,
                               double w_p, float* confidence, void* stream);
+
+/*
+ * Norms and rotary positions of queries and keys, in one pass: the tensors
+ * that a model's projections give become the q, k_new of confkv_step, or the
+ * q, k of a prompt.  The paper has no counterpart.  Per token and head:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight     (without a weight: y = x)
+ *   (a, b) -> mscale (a cos t - b sin t, b cos t + a sin t)
+ * for the pairs of the first rot channels, (2i, 2i + 1) if `interleaved`,
+ * else (i, i + rot / 2), with t = 2 pi * position * turns[i] / 2^64.  Channels
+ * from rot on are not rotated.  All arithmetic is fp32 (angles exact modulo
+ * one turn), rounded once to the output type.
+ *   q [n][Hq][d], k [n][Hkv][d] in in_dtype; q_out, k_out the same shapes in
+ *   their own types; any of fp16, bf16, fp32.  Strides in elements, token
+ *   first, then head; channels contiguous, addresses aligned to the element.
+ *   Hkv = 0: no keys (k, k_out ignored).  An output may be its input (same
+ *   address, strides and type); otherwise outputs must overlap nothing.
+ *   q_weight, k_weight: [d] in w_dtype, or NULL (no norm for that tensor)
+ *   positions: device int32 [n]; turns: device [rot / 2], from
+ *   confkv_rotary_frequencies; both may be NULL if rot = 0
+ * d up to 512 (CONFKV_ENOTIMPL above).  Fast for d = 64, 128, 256 with rot a
+ * multiple of 16 and every row on a 16-byte boundary.  Asynchronous on
+ * `stream`, may be captured.
+ */
+typedef struct confkv_rotary_args {
+  int32_t n, Hq, Hkv, d, rot;
+  int32_t interleaved;
+  int32_t in_dtype, w_dtype, q_out_dtype, k_out_dtype;
+  float eps, mscale;
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t q_stride[2], k_stride[2], q_out_stride[2], k_out_stride[2];
+  const void *q_weight, *k_weight;
+  const int32_t* positions;
+  const uint64_t* turns;
+} confkv_rotary_args;
+int confkv_qk_rotary(const confkv_rotary_args* args, void* stream);
+
+/* Frequencies of the rot / 2 pairs as turns per position in units of 2^-64
+ * (HOST array `turns`), and the factor of the rotated channels.  Pair i turns
+ * by f_i = base^(-2i / rot) radians per position (base > 1);
+ *   CONFKV_ROTARY_LINEAR  f_i / factor
+ *   CONFKV_ROTARY_NTK     base * factor^(rot / (rot - 2)) in place of base
+ *   CONFKV_ROTARY_YARN    (arXiv 2309.00071) with r = original_length f_i /
+ *       (2 pi) turns in the trained length, g = clamp((r - beta_slow) /
+ *       (beta_fast - beta_slow), 0, 1): f_i g + f_i / factor (1 - g), and
+ *       mscale = 0.1 ln(factor) + 1 (1 otherwise)
+ * factor >= 1.  Host only. */
+enum { CONFKV_ROTARY_PLAIN = 0, CONFKV_ROTARY_LINEAR = 1, CONFKV_ROTARY_NTK = 2, CONFKV_ROTARY_YARN = 3 };
+int confkv_rotary_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original_length,
+                              double beta_fast, double beta_slow, uint64_t* turns, float* mscale);
+
+/*
+ * Attention of packed prompts.  The paper has no counterpart: its decode step
+ * starts from a prefilled cache, and this is the attention that produces the
+ * prefill's own hidden states, for a whole prompt, a chunk of one against its
+ * history, or single tokens.  Sequence b of B holds query rows
+ * cu_q[b] .. cu_q[b+1]-1 of q and key rows cu_k[b] .. cu_k[b+1]-1 of k and v:
+ *   out[i][h] = sum_j softmax_j(scale q[i][h] . k[j][h / G]) v[j][h / G],
+ *   lse[i][h] = log sum_j exp(scale q[i][h] . k[j][h / G]),   G = Hq / Hkv,
+ * over all keys of the sequence, or with `causal` over those up to the
+ * query's own position, the queries being the last of the sequence: query i
+ * of lq sees keys 0 .. lk - lq + i.  A row that sees no key gets out = 0 and
+ * lse = -inf.
+ *   q [total_q][Hq][d], k, v [total_k][Hkv][d], out [total_q][Hq][d], all
+ *   fp16 or all bf16 (dtype), d = 64 or 128.  Strides are in elements, token
+ *   first, then head; channels are contiguous.  Every base address is a
+ *   multiple of 16 bytes, every stride of 8 elements and at least d.
+ *   lse: fp32 [total_q][Hq], or NULL.
+ *   cu_q, cu_k: DEVICE int32 [B + 1], ascending from 0; values outside
+ *   [0, total] are clamped to it.  Rows of out and lse that belong to no
+ *   sequence are not written.
+ * Scores, maxima, sums and the accumulated output are fp32; the weights are
+ * rounded to `dtype` for the product with v, the output once at the end.
+ * Values of keys that no query of the call sees do not reach the output,
+ * NaN and infinities among them; a non-finite value of v within a sequence
+ * may reach rows up to 127 keys before it.  out must not overlap an input.
+ * The call uses no workspace and may be captured.  Asynchronous on `stream`.
+ * CONFKV_EINVAL for a bad argument, CONFKV_ENOTIMPL for another d.
+ */
+typedef struct confkv_prompt_args {
+  int32_t B, Hq, Hkv, d;
+  int32_t dtype;              /* CONFKV_Q_FP16 or CONFKV_Q_BF16 */
+  int32_t causal;
+  int32_t total_q, total_k;
+  float scale;                /* > 0 */
+  int32_t reserved;           /* 0 */
+  const void *q, *k, *v;
+  void* out;
+  float* lse;
+  const int32_t *cu_q, *cu_k;
+  int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];
+} confkv_prompt_args;
+int confkv_prompt_attention(const confkv_prompt_args* args, void* stream);
+
+/* Whether a bounded wait of a confkv_prompt_attention kernel gave up on the
+ * current device since the last call (CONFKV_STATUS_TIMEOUT in `bits`, and
+ * CONFKV_EDEVICE): outputs of the calls since then are not valid.
+ * Synchronises `stream` and clears the word. */
+int confkv_prompt_status(int32_t* bits, void* stream);
 
 /* Human-readable text of a status code. */
 const char* confkv_status_string(int status);
