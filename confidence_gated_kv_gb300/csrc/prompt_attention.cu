@@ -26,8 +26,7 @@ using namespace tc;
 constexpr int kRows = 128;               // score rows per tile
 constexpr int kKeys = 128;               // keys per tile
 constexpr int kThreads = 384;            // two softmax warpgroups, one for copies and products
-constexpr long long kPolls = 1LL << 21;  // polls per wait (a few seconds at most)
-constexpr uint32_t kPollNs = 1000;
+constexpr int kPolls = 1 << 24;          // polls per wait (a few seconds at most)
 
 template <int D>
 struct Tile {
@@ -52,8 +51,7 @@ struct Args {
 struct Item {                            // what one CTA computes
   int q0, lq, k0, lk;                    // packed rows and lengths of the sequence
   int t0, head;                          // first token (within the sequence), KV head
-  int n[2];                              // key tiles of each row tile
-  int active[2];
+  int n0, n1;                            // key tiles of each row tile
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -87,17 +85,27 @@ __device__ bool find_item(const Args& a, int tile, int head, Item* it) {
         const int t0 = (nt - 1 - (tile - (before + sum - nt))) * per;   // the longest rows first
         it->q0 = q0; it->lq = lq; it->k0 = k0; it->lk = lk;
         it->t0 = t0; it->head = head;
-        for (int w = 0; w < 2; ++w) {
-          const int ta = t0 + w * a.tokens, te = min(ta + a.tokens, lq);
-          it->active[w] = ta < lq;
-          const int seen = a.causal ? clampi(lk - lq + te, 0, lk) : lk;
-          it->n[w] = ta < lq ? (seen + kKeys - 1) / kKeys : 0;
-        }
+        const int mid = min(t0 + a.tokens, lq), end = min(t0 + per, lq);
+        const int seen0 = a.causal ? clampi(lk - lq + mid, 0, lk) : lk;
+        const int seen1 = a.causal ? clampi(lk - lq + end, 0, lk) : lk;
+        it->n0 = (seen0 + kKeys - 1) / kKeys;
+        it->n1 = end > mid ? (seen1 + kKeys - 1) / kKeys : 0;
       }
       return true;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
+  return false;
+}
+
+// Bounded wait; false once it, or another wait of the CTA, has given up.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  for (int i = 0; i < kPolls; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  atomicOr(status, kStatusTimeout);
   return false;
 }
 
@@ -109,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kHalf = kRows * 128;                    // one 64-channel column block of a tile
   constexpr uint32_t kTmem = 512, kOut = 256;           // scores at 0 and 128, outputs from 256
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * Tile<D>::kStages + 10];
+  __shared__ __align__(8) uint64_t s_bar[2 * Tile<D>::kStages + 13];
   __shared__ Item s_item;
   __shared__ uint32_t s_tmem;
   __shared__ int s_found;
@@ -124,9 +132,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rest = bar0 + 16u * kStages;
   auto q_full = [&](int w) { return rest + 8u * w; };
   auto s_full = [&](int w) { return rest + 16u + 8u * w; };
-  auto p_full = [&](int w) { return rest + 32u + 8u * w; };
-  auto o_full = [&](int w) { return rest + 48u + 8u * w; };
-  const uint32_t v_last = rest + 64u, drained = rest + 72u;
+  auto p_full = [&](int w, int half) { return rest + 32u + 16u * w + 8u * half; };
+  auto o_full = [&](int w) { return rest + 64u + 8u * w; };
+  const uint32_t v_last = rest + 80u;
+  auto drained = [&](int w) { return rest + 88u + 8u * w; };
 
   if (warp == 8) tmem_alloc(smem_addr(&s_tmem), kTmem);
   if (warp == 9) {
@@ -137,16 +146,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     for (int s = 0; s < kStages; ++s) {
       bar_init(full(s), 1);
-      bar_init(empty(s), 1);
+      bar_init(empty(s), 2);
     }
     for (int w = 0; w < 2; ++w) {
       bar_init(q_full(w), 1);
       bar_init(s_full(w), 1);
-      bar_init(p_full(w), kRows);
+      bar_init(p_full(w, 0), kRows);
+      bar_init(p_full(w, 1), kRows);
       bar_init(o_full(w), 1);
+      bar_init(drained(w), 1);
     }
     bar_init(v_last, 1);
-    bar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
@@ -156,83 +166,101 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = s_tmem;
-  const Item it = s_item;
   const bool found = s_found != 0;
-  const int n = found ? max(it.n[0], it.n[1]) : 0;
-  const bool partial = n * kKeys > it.lk;               // the last key tile ends behind the sequence
 
-  // Bounded wait; false once it, or another wait of the CTA, has given up.
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    for (long long i = 0; i < kPolls; ++i) {
-      if (bar_try(bar, parity, kPollNs)) return true;
-      if (s_abort) return false;
-    }
-    s_abort = 1;
-    if (a.status) atomicOr(a.status, kStatusTimeout);
-    return false;
-  };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_on(bar, parity, &s_abort, a.status); };
 
   if (warp >= 8) {
     regs_dec<80>();
-    if (warp == 8 && lane == 0 && n > 0) {
+    const Item it = s_item;
+    const int n = found ? max(it.n0, it.n1) : 0;
+    const bool partial = n * kKeys > it.lk;             // the last key tile ends behind the sequence
+    if ((warp == 8 || warp == 11) && n > 0) {
       // ---------------------------------------------------------- products
+      // A warp per row tile: a warp that has issued products goes on to its
+      // next wait only when they are done, so one warp for both tiles leaves
+      // the tensor cores idle between them.  The whole warp runs the role,
+      // one lane issues.
       constexpr uint32_t dqk = mma_desc(kRows, kKeys, BF16, false), dpv = mma_desc(kRows, D, BF16, true);
-      auto issue_s = [&](int w, int stage) {
-        const uint32_t qa = sq + w * kBytes, ka = skv + stage * kBytes;
+      const int w = warp == 11, nw = w ? it.n1 : it.n0;
+      const uint32_t scores = tmem + w * kKeys, output = tmem + kOut + w * D, q = desc_lo(sq + w * kBytes, 16);
+      auto issue_s = [&](int stage) {
+        const uint32_t k = desc_lo(skv + stage * kBytes, 16);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-          mma_ss(tmem + w * kKeys, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), dqk, k > 0);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+          mma_ss(scores, q + off, k + off, desc_hi(1024), dqk, i > 0);
         }
-      };
-      auto issue_o = [&](int w, int stage, bool accumulate) {
-        const uint32_t va = skv + stage * kBytes;
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + kOut + w * D, tmem + w * kKeys + 8 * k, smem_desc(va + k * 2048, kHalf, 1024), dpv,
-                 accumulate || k > 0);
-      };
-      bool ok = wait(full(0), 0);
-      for (int w = 0; w < 2 && ok; ++w) {
-        if (it.n[w] == 0) continue;
-        ok = wait(q_full(w), 0);
-        if (!ok) break;
-        fence_after();
-        issue_s(w, 0);
         mma_commit(s_full(w));
+      };
+      auto issue_o = [&](int stage, int half, bool accumulate) {
+        const uint32_t v = desc_lo(skv + stage * kBytes + half * (kHalf / 2), kHalf);
+        const uint32_t p = scores + half * (kKeys / 4);
+#pragma unroll
+        for (int i = 0; i < kKeys / 32; ++i)
+          mma_ts(output, p + 8 * i, v + i * (2048 >> 4), desc_hi(1024), dpv, accumulate || half > 0 || i > 0);
+      };
+      auto all = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(bar, parity)); };
+      bool ok = true;
+      int stage = -1;                                   // the latest tile of the ring and its parity
+      uint32_t parity = 0;
+      auto next_full = [&] {
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+        ok = ok && all(full(stage), parity);
+      };
+      if (nw > 0) {
+        next_full();
+        ok = ok && all(q_full(w), 0);
+        if (ok) {
+          fence_after();
+          if (elect()) {
+            issue_s(0);
+            mma_commit(empty(0));
+          }
+          __syncwarp();
+        }
       }
-      if (ok) mma_commit(empty(0));
-      for (int j = 0; j < n && ok; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kStages, sk = ik % kStages;
-        ok = wait(full(sv), (iv / kStages) & 1);
-        if (ok && j + 1 < n) ok = wait(full(sk), (ik / kStages) & 1);
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (j >= it.n[w]) continue;
-          ok = wait(p_full(w), j & 1);
+      for (int j = 0; j < nw && ok; ++j) {
+        next_full();                                    // V of this tile
+        const int v = stage;
+        if (j + 1 < nw) next_full();                    // K of the next one
+        const int k = stage;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && all(p_full(w, half), j & 1);
           if (!ok) break;
           fence_after();
-          issue_o(w, sv, j > 0);
-          if (j + 1 < it.n[w]) {
-            issue_s(w, sk);
-            mma_commit(s_full(w));
-          } else {
-            mma_commit(o_full(w));
+          if (elect()) {
+            issue_o(v, half, j > 0);
+            if (half) {
+              if (j + 1 < nw) {
+                issue_s(k);
+                mma_commit(empty(k));
+              } else {
+                mma_commit(o_full(w));
+              }
+              mma_commit(empty(v));
+            }
           }
-        }
-        if (ok) {
-          mma_commit(empty(sv));
-          if (j + 1 < n) mma_commit(empty(sk));
+          __syncwarp();
         }
       }
-      if (!ok) {                                        // nothing in flight when the CTA ends
-        mma_commit(drained);
-        for (long long i = 0; i < kPolls && !bar_try(drained, 0, kPollNs); ++i) {}
+      for (int i = 2 * nw; i < 2 * n && ok; ++i) {      // tiles that only the other row tile sees
+        next_full();
+        if (ok && lane == 0) bar_arrive(empty(stage));
+      }
+      if (!ok && elect()) {                             // nothing in flight when the CTA ends
+        mma_commit(drained(w));
+        for (int i = 0; i < kPolls && !bar_try(drained(w), 0); ++i) {}
       }
     } else if (warp == 9 && lane == 0 && n > 0) {
       // ---------------------------------------------------------- copies
       const int q_bytes = a.tokens * a.G * D * 2;
       auto load_q = [&](int w) {
-        if (it.n[w] == 0) return;
+        if ((w ? it.n1 : it.n0) == 0) return;
         bar_expect(q_full(w), q_bytes);
         for (int c = 0; c < D / 64; ++c)
           tma_load(sq + w * kBytes + c * kHalf, &map_q, c * 64, it.head * a.G, it.q0 + it.t0 + w * a.tokens,
@@ -254,12 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         for (int w = 0; w < 2; ++w)
-          if (it.n[w])
-            for (long long i = 0; i < kPolls && !bar_try(q_full(w), 0, kPollNs); ++i) {}
+          if (w ? it.n1 : it.n0)
+            for (int i = 0; i < kPolls && !bar_try(q_full(w), 0); ++i) {}
         for (int j = max(0, issued - kStages); j < issued; ++j) {
           const bool last = partial && j == 2 * n - 1;
-          for (long long i = 0; i < kPolls && !bar_try(last ? v_last : full(j % kStages),
-                                                       last ? 0 : (j / kStages) & 1, kPollNs); ++i) {}
+          for (int i = 0; i < kPolls && !bar_try(last ? v_last : full(j % kStages),
+                                                       last ? 0 : (j / kStages) & 1); ++i) {}
         }
       }
     } else if (warp == 10 && n > 0 && partial) {
@@ -283,8 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<208>();
+    const Item it = s_item;
     const int w = warp >> 2, row = threadIdx.x & 127;
-    if (found && it.active[w]) {
+    const int nw = w ? it.n1 : it.n0;                   // key tiles of this row tile
+    if (found && it.t0 + w * a.tokens < it.lq) {
       const int t = it.t0 + w * a.tokens + row / a.G;
       const bool valid = row < a.tokens * a.G && t < it.lq;
       const int seen = !valid ? 0 : a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
@@ -292,27 +322,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ts = tmem + w * kKeys + lane_base, to = tmem + kOut + w * D + lane_base;
       float ref = -INFINITY, l = 0.f;                   // reference of the exponentials, their sum
       bool ok = true;
-      for (int j = 0; j < it.n[w]; ++j) {
+      for (int j = 0; j < nw; ++j) {
         ok = __all_sync(0xffffffffu, wait(s_full(w), j & 1));
         if (!ok) break;
         fence_after();
-        uint32_t s[kKeys];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
-        wait_ld();
         const int left = seen - j * kKeys;              // keys of the tile that the row sees
-        if (__any_sync(0xffffffffu, left < kKeys)) {
+        const bool masked = __any_sync(0xffffffffu, left < kKeys);
+        uint32_t s[kKeys];
+        float m[4] = {ref, ref, ref, ref};
+        tmem_ld32(ts, s);
+        wait_ld32(s);
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (c >= left) s[c] = 0xff800000u;
-        }
-        float m0 = __uint_as_float(s[0]), m1 = __uint_as_float(s[1]);
+        for (int c = 0; c < kKeys; c += 32) {           // the maximum of a quarter while the next one loads
+          if (c + 32 < kKeys) tmem_ld32(ts + c + 32, s + c + 32);
+          if (masked) {
 #pragma unroll
-        for (int c = 2; c < kKeys; c += 2) {
-          m0 = fmaxf(m0, __uint_as_float(s[c]));
-          m1 = fmaxf(m1, __uint_as_float(s[c + 1]));
+            for (int i = 0; i < 32; ++i)
+              if (c + i >= left) s[c + i] = 0xff800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            m[i / 2 % 4] = fmaxf(fmaxf(__uint_as_float(s[c + i]), __uint_as_float(s[c + i + 1])), m[i / 2 % 4]);
+          if (c + 32 < kKeys) wait_ld32(s + c + 32);
         }
-        const float top = fmaxf(fmaxf(m0, m1), ref);
+        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         // The reference moves only when it would be passed by more than 2^8:
         // the weights then stay below 2^8, and the accumulator in tensor
         // memory is rarely rescaled.  The product that reads it is done:
@@ -322,38 +355,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = move && top > ref ? ex2((ref - top) * a.scale2) : 1.f;
           l *= f;
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + c, o);
-            wait_ld();
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
+            wait_ld16(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(to + c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(to + c, o);
           }
-          wait_st();
         }
         if (move) ref = top;
         const float base = ref == -INFINITY ? 0.f : -ref * a.scale2;
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t scale_pair = pair(a.scale2, a.scale2), base_pair = pair(base, base);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 64) {
-          uint32_t p[32];
+        for (int c = 0; c < kKeys; c += 32) {           // a quarter of the weights at a time
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = ex2(fmaf(__uint_as_float(s[c + 2 * i]), a.scale2, base));
-            const float y = ex2(fmaf(__uint_as_float(s[c + 2 * i + 1]), a.scale2, base));
-            l0 += x;
-            l1 += y;
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpair(fma2(pair(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), scale_pair, base_pair),
+                   x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[i & 1] = add2(sum[i & 1], pair(x, y));
             p[i] = pack2<BF16>(x, y);
           }
-          tmem_st32(ts + c / 2, p);
+          tmem_st16(ts + c / 2, p);
+          if (c & 32) {                                 // the product starts with the first half
+            wait_st();
+            fence_before();
+            bar_arrive(p_full(w, c / 64));
+          }
         }
+        float l0, l1;
+        unpair(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
-        wait_st();
-        fence_before();
-        bar_arrive(p_full(w));
       }
-      if (ok && it.n[w] > 0) {
+      if (ok && nw > 0) {
         ok = __all_sync(0xffffffffu, wait(o_full(w), 0));
         fence_after();
       }
@@ -365,9 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          if (it.n[w] > 0) {
+          if (nw > 0) {
             tmem_ld32(to + c, o);
-            wait_ld();
+            wait_ld32(o);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

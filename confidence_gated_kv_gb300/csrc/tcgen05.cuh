@@ -22,14 +22,13 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// One poll of a phase; the thread may sleep in it for up to `ns`.
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity, uint32_t ns) {
+// One poll of a phase (the hardware may let the thread sleep for a while).
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(ns)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -59,10 +58,9 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {    
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-#define CONFKV_R4(a, i) a[i], a[i + 1], a[i + 2], a[i + 3]
+#define CONFKV_IO4(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3])
 #define CONFKV_OUT4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
 #define CONFKV_IN4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
 // 32 consecutive columns of the warp's 32 lanes, one lane per thread.
@@ -76,16 +74,36 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-      "%29,%30,%31};\n" ::CONFKV_IN4(r, 0),
-      CONFKV_IN4(r, 4), CONFKV_IN4(r, 8), CONFKV_IN4(r, 12), CONFKV_IN4(r, 16), CONFKV_IN4(r, 20), CONFKV_IN4(r, 24),
-      CONFKV_IN4(r, 28), "r"(addr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : CONFKV_OUT4(r, 0), CONFKV_OUT4(r, 4), CONFKV_OUT4(r, 8), CONFKV_OUT4(r, 12)
+      : "r"(addr)
       : "memory");
 }
-#undef CONFKV_R4
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::CONFKV_IN4(r, 0),
+      CONFKV_IN4(r, 4), CONFKV_IN4(r, 8), CONFKV_IN4(r, 12), "r"(addr)
+      : "memory");
+}
+// Waits for the loads so far.  The registers are operands, so that nothing
+// that reads them is moved up across the wait.
+__device__ __forceinline__ void wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : CONFKV_IO4(r, 0), CONFKV_IO4(r, 4), CONFKV_IO4(r, 8), CONFKV_IO4(r, 12), CONFKV_IO4(r, 16),
+                 CONFKV_IO4(r, 20), CONFKV_IO4(r, 24), CONFKV_IO4(r, 28)
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : CONFKV_IO4(r, 0), CONFKV_IO4(r, 4), CONFKV_IO4(r, 8), CONFKV_IO4(r, 12)
+               :
+               : "memory");
+}
+#undef CONFKV_IO4
 #undef CONFKV_OUT4
 #undef CONFKV_IN4
 
@@ -95,35 +113,49 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 // 8-row groups, `block` that of consecutive 64-element column blocks of an
 // operand whose contiguous axis is M or N (not read for one whose contiguous
 // axis is K, where a K step advances inside the 128-byte row).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t block, uint32_t group) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// The address is in the low word, in units of 16 bytes; the high word is the
+// same for every tile.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t block) {
+  return ((addr & 0x3FFFF) >> 4) | ((block >> 4) << 16);
 }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t group) { return (group >> 4) | (1u << 14) | (2u << 29); }
 // Instruction descriptor of kind::f16: fp32 accumulators, A and B both fp16
 // or both bf16, A with contiguous K, B with contiguous K or N.
 __host__ __device__ constexpr uint32_t mma_desc(int M, int N, bool bf16, bool b_n_contiguous) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_n_contiguous ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D[tensor memory] (+)= A[shared] * B[shared]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+// D[tensor memory] (+)= A[shared] * B[shared]; low words of the descriptors,
+// whose high word is `hi`.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t desc,
+                                       bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(desc), "r"((uint32_t)accumulate)
       : "memory");
 }
 // D[tensor memory] (+)= A[tensor memory] * B[shared]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t desc,
+                                       bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.u32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(desc), "r"((uint32_t)accumulate)
       : "memory");
 }
 // Arrives on `bar` once every tcgen05 operation this thread issued so far is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
+// True in one lane of a converged warp, always the same one: the code that
+// it guards is issued once, from uniform registers.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one)::"memory");
+  return one != 0;
 }
 
 // ------------------------------------------------------------- registers
@@ -136,6 +168,30 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 // Two fp32 values as fp16 or bf16 pairs, `lo` in the low half.
 template <bool BF16>
