@@ -178,13 +178,18 @@ def dtype_code(dtype) -> int:
 
 
 _same = contextlib.nullcontext()
+_current_device = None
 
 
-def on_device(dev):
-    """Context in which `dev` is the current device (launches go to the
-    current one); nothing to do when it already is."""
+def on_device(index: int):
+    """Context in which device `index` is the current one (launches go to the
+    current device); nothing to do when it already is."""
+    global _current_device
     import torch
-    return _same if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if _current_device is None:
+        torch.cuda.init()
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _same if index == _current_device() else torch.cuda.device(index)
 
 
 _raw_stream_fn = None
@@ -300,17 +305,20 @@ class Cache:
         ints).  Write every layer with prefill_layer, then step."""
         if len(prefill_len) != self.B:
             raise ValueError("prefill_len: one length per sequence is wanted")
-        with on_device(self.device):
+        with on_device(self._dev_index):
             _check(lib().confkv_prefill_begin(self._h, struct.pack("=%di" % self.B, *prefill_len),
                                               _stream(stream, self._dev_index)), "confkv_prefill_begin")
         self._prompt_rows = sum(prefill_len)
 
     def _packed(self, t, name, rows):
-        """Checks a packed [rows, Hkv, d] tensor of this cache's device."""
-        if t.dim() != 3 or tuple(t.shape[1:]) != (self.Hkv, self.d) or t.shape[0] != rows or t.stride(2) != 1:
+        """Address and strides of a packed [rows, Hkv, d] tensor of this
+        cache's device."""
+        stride = t.stride()
+        if t.shape != (rows, self.Hkv, self.d) or stride[2] != 1:
             raise ValueError("%s: [%d, %d, %d] with contiguous channels is wanted" % (name, rows, self.Hkv, self.d))
-        if t.device.type != "cuda" or t.device.index != self._dev_index:
+        if t.get_device() != self._dev_index:
             raise ValueError("%s is on %s, not on the cache's device" % (name, t.device))
+        return t.data_ptr(), _PAIR.pack(stride[0], stride[1])
 
     def prefill_layer(self, layer: int, k, v, stream=None):
         """K/V of one layer for all sequences, [rows, Hkv, d] fp16 or bf16, the
@@ -318,21 +326,22 @@ class Cache:
         rows = getattr(self, "_prompt_rows", None)
         if rows is None:
             raise ConfkvError(ESTATE, "prefill_layer before prefill_begin")
-        self._packed(k, "k", rows)
-        self._packed(v, "v", rows)
+        k_at, ks = self._packed(k, "k", rows)
+        v_at, vs = self._packed(v, "v", rows)
         if k.dtype != v.dtype:
             raise ValueError("k and v: one type is wanted")
-        with on_device(self.device):
-            _check(lib().confkv_prefill_layer(self._h, int(layer), k.data_ptr(), v.data_ptr(), dtype_code(k.dtype),
-                                              _PAIR.pack(*k.stride()[:2]), _PAIR.pack(*v.stride()[:2]),
-                                              _stream(stream, self._dev_index)), "confkv_prefill_layer")
+        with on_device(self._dev_index):
+            st = lib().confkv_prefill_layer(self._h, layer, k_at, v_at, dtype_code(k.dtype), ks, vs,
+                                            _stream(stream, self._dev_index))
+        if st:
+            _check(st, "confkv_prefill_layer")
 
     def read_rows(self) -> int:
         """Rows that always hold a layer's resident entries (exact until the
         first step)."""
         n = ctypes.c_int64()
         _check(lib().confkv_read_rows(self._h, ctypes.byref(n)), "confkv_read_rows")
-        return int(n.value)
+        return n.value
 
     def read_layer(self, layer: int, dtype=None, out=None, stream=None) -> dict:
         """Resident entries of one layer: dict of k, v [rows, Hkv, d]
@@ -341,25 +350,29 @@ class Cache:
         and type.  Sequence b has rows cu_seqlens[b] to cu_seqlens[b + 1]."""
         import torch
         if out is None:
-            n, dev, dt = self.read_rows(), self.device, torch.float16 if dtype is None else dtype
-            out = dict(k=torch.empty((n, self.Hkv, self.d), dtype=dt, device=dev),
-                       v=torch.empty((n, self.Hkv, self.d), dtype=dt, device=dev),
-                       positions=torch.empty(n, dtype=torch.int32, device=dev),
-                       cu_seqlens=torch.empty(self.B + 1, dtype=torch.int32, device=dev))
-        k, v, pos, cu = out["k"], out["v"], out["positions"], out["cu_seqlens"]
-        rows = k.shape[0]
-        self._packed(k, "k", rows)
-        self._packed(v, "v", rows)
-        if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
-            raise ValueError("k and v: one type is wanted")
-        for name, t, n in (("positions", pos, rows), ("cu_seqlens", cu, self.B + 1)):
-            if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != k.device:
-                raise ValueError("%s: a contiguous int32 vector of %d on the cache's device is wanted" % (name, n))
-        with on_device(self.device):
-            _check(lib().confkv_read_layer(self._h, int(layer), dtype_code(k.dtype), k.data_ptr(), v.data_ptr(),
-                                           _PAIR.pack(*k.stride()[:2]), _PAIR.pack(*v.stride()[:2]), pos.data_ptr(),
-                                           cu.data_ptr(), rows, _stream(stream, self._dev_index)),
-                   "confkv_read_layer")
+            rows, ws = self.read_rows(), self.workspace
+            shape, dt = (rows, self.Hkv, self.d), torch.float16 if dtype is None else dtype
+            k, v = ws.new_empty(shape, dtype=dt), ws.new_empty(shape, dtype=dt)
+            pos = ws.new_empty((rows,), dtype=torch.int32)
+            cu = ws.new_empty((self.B + 1,), dtype=torch.int32)
+            out = {"k": k, "v": v, "positions": pos, "cu_seqlens": cu}
+            k_at, v_at, ks = k.data_ptr(), v.data_ptr(), _PAIR.pack(self.Hkv * self.d, self.d)
+            vs = ks
+        else:
+            k, v, pos, cu = out["k"], out["v"], out["positions"], out["cu_seqlens"]
+            rows = k.shape[0]
+            k_at, ks = self._packed(k, "k", rows)
+            v_at, vs = self._packed(v, "v", rows)
+            if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
+                raise ValueError("k and v: one type is wanted")
+            for name, t, n in (("positions", pos, rows), ("cu_seqlens", cu, self.B + 1)):
+                if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != k.device:
+                    raise ValueError("%s: a contiguous int32 vector of %d on the cache's device is wanted" % (name, n))
+        with on_device(self._dev_index):
+            st = lib().confkv_read_layer(self._h, layer, dtype_code(k.dtype), k_at, v_at, ks, vs, pos.data_ptr(),
+                                         cu.data_ptr(), rows, _stream(stream, self._dev_index))
+        if st:
+            _check(st, "confkv_read_layer")
         return out
 
     def new_outputs(self):

@@ -29,9 +29,8 @@ namespace confkv {
 namespace {
 
 constexpr int kChunk = 528;          // shared-memory pitch of a 512-byte piece of an interleaved block
-constexpr int kWriteWarps = 16;
+constexpr int kWriteWarps = 8;
 constexpr int kReadWarps = 8;
-constexpr int kReadBlocks = 2;       // 16-token blocks per warp of the read kernel
 
 // ------------------------------------------------------------------ reset
 
@@ -60,110 +59,122 @@ __global__ void prefill_reset_kernel(Shape s, Dev d, LengthChunk c) {
 
 // ------------------------------------------------------------------ write
 
-// 8 source values as fp16 pairs.
-__device__ __forceinline__ uint4 load_half8(const uint16_t* p, bool bf16) {
-  uint4 u = *reinterpret_cast<const uint4*>(p);
-  if (bf16) {
-    uint32_t* w = &u.x;
+// Two source values as fp16 (an overflow becomes infinite).
+template <bool BF16>
+__device__ __forceinline__ __half2 half_pair(uint32_t w) {
+  if (BF16) return __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return *reinterpret_cast<const __half2*>(&w);
+}
+
+// Larger absolute value of each half of two words; a NaN loses.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs(uint32_t top, uint32_t w) {
+  w &= 0x7fff7fffu;
+  if (BF16) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&w));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&top), *reinterpret_cast<const __half2*>(&w));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// Stored bytes of 8 values: clamp(rint(x / s), -127, 127) + 128, with the
+// IEEE quotient.  x * (1 / s) is within 2 ulp of it (2^-15 up to 127), so the
+// integers agree unless the product lies that close to a half; only then, or
+// for a NaN, are the quotients computed.  Adding 1.5 2^23 + 128 rounds to an
+// integer (ties to even) and leaves the stored byte in the low bits.  No
+// clamp: |x| <= 127 s (1 + 2^-23).
+__device__ __forceinline__ uint2 quantise8(const __half2 (&x)[4], const float (&scale)[8], const float (&inv)[8]) {
+  constexpr float kRound = 12582912.f + 128.f;
+  uint32_t r[8];
+  bool near = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(x[j]);
+    const float q0 = f.x * inv[2 * j], q1 = f.y * inv[2 * j + 1];
+    const float r0 = q0 + kRound, r1 = q1 + kRound;
+    near = near || !(fabsf(q0 - (r0 - kRound)) <= 0.49993f) || !(fabsf(q1 - (r1 - kRound)) <= 0.49993f);
+    r[2 * j] = __float_as_uint(r0);
+    r[2 * j + 1] = __float_as_uint(r1);
+  }
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(x[j]);
+      r[2 * j] = (int)fminf(fmaxf(rintf(__fdiv_rn(f.x, scale[2 * j])), -127.f), 127.f) + kCodeBias;
+      r[2 * j + 1] = (int)fminf(fmaxf(rintf(__fdiv_rn(f.y, scale[2 * j + 1])), -127.f), 127.f) + kCodeBias;
     }
   }
-  return u;
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(r[4], r[5], 0x0040), __byte_perm(r[6], r[7], 0x0040), 0x5410);
+  return o;
 }
 
-// clamp(rint(x / s), -127, 127) with the IEEE quotient.  x * (1 / s) is
-// within 2 ulp of it (below 2^-15 up to 127), so the integers agree unless
-// the product lies that close to a half; only then is the quotient computed.
-__device__ __forceinline__ int quantise(float x, float s, float inv) {
-  float q = x * inv;
-  if (fabsf(fabsf(q - truncf(q)) - 0.5f) < 6.1e-5f) q = __fdiv_rn(x, s);
-  return (int)fminf(fmaxf(rintf(q), -127.f), 127.f);
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWriteWarps * 32, 2)
-    write_layer_kernel(Shape s, Dev d, int layer, int bf16, const uint16_t* __restrict__ k,
-                       const uint16_t* __restrict__ v, long long k_t, long long k_h, long long v_t, long long v_h) {
+template <int D, bool BF16, bool IS_V>
+__device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int layer, int b, int h,
+                                           const uint16_t* __restrict__ src, long long ts, uint8_t* smem,
+                                           uint32_t* s_abs) {
   constexpr int kPer = D / 8;                          // threads per row
   constexpr int kRowsAtOnce = kWriteWarps * 32 / kPer;
-  extern __shared__ __align__(16) uint8_t smem[];      // an interleaved block per warp
-  __shared__ uint32_t s_abs[D / 2];                    // absmax of this CTA's tokens, fp16 pairs
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
-  const int unit = blockIdx.x / ctas;                  // (sequence, KV head, K or V)
-  const bool is_v = unit & 1;
-  const int h = (unit >> 1) % s.Hkv, b = (unit >> 1) / s.Hkv;
   const int T0 = d.T0[b], n8 = max(0, T0 - s.W);
-  const uint16_t* src = is_v ? v : k;
-  const long long ts = is_v ? v_t : k_t;
-  src += d.row0[b] * ts + h * (is_v ? v_h : k_h);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ch = threadIdx.x % kPer;                   // 8-channel chunk of this thread
   const size_t lb = lb_index(s, layer, b), u = unit_index(s, layer, b, h);
+  auto row = [&](long long t) { return *reinterpret_cast<const uint4*>(src + t * ts + ch * 8); };
 
-  for (int i = threadIdx.x; i < D / 2; i += blockDim.x) s_abs[i] = 0;
-  __syncthreads();
-  // ---- absmax over the CTA's share of the tokens
-  __half2 top[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top[i] = __float2half2_rn(0.f);
+  // ---- absmax over the CTA's share of the tokens (fp16 rounding keeps the
+  // order, so bf16 maxima are converted at the end)
+  uint32_t top[4] = {0, 0, 0, 0};
   {
     const int per = (T0 + ctas - 1) / ctas, t1 = min(T0, (rank + 1) * per);
     int t = rank * per + threadIdx.x / kPer;
-    for (; t + 3 * kRowsAtOnce < t1; t += 4 * kRowsAtOnce) {
-      uint4 x[4];
+    for (; t + 7 * kRowsAtOnce < t1; t += 8 * kRowsAtOnce) {
+      uint4 x[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = load_half8(src + (t + i * kRowsAtOnce) * ts + ch * 8, bf16);
+      for (int i = 0; i < 8; ++i) x[i] = row(t + i * kRowsAtOnce);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2* w = reinterpret_cast<const __half2*>(&x[i]);
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top[j] = __hmax2(top[j], __habs2(w[j]));
-      }
+        for (int j = 0; j < 4; ++j) top[j] = max_abs<BF16>(top[j], (&x[i].x)[j]);
     }
     for (; t < t1; t += kRowsAtOnce) {
-      const uint4 x = load_half8(src + t * ts + ch * 8, bf16);
-      const __half2* w = reinterpret_cast<const __half2*>(&x);
+      const uint4 x = row(t);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top[j] = __hmax2(top[j], __habs2(w[j]));
+      for (int j = 0; j < 4; ++j) top[j] = max_abs<BF16>(top[j], (&x.x)[j]);
     }
   }
 #pragma unroll
   for (int o = kPer; o < 32; o <<= 1)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top[j] = __hmax2(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-  // fp16 absolute values order like their bits, so each half can be merged
-  // as an integer: one lane per chunk and warp, one 32-bit word per pair
-  __half2* stage = reinterpret_cast<__half2*>(smem);   // [warp][D / 2]
+    for (int j = 0; j < 4; ++j) top[j] = max_abs<BF16>(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+  uint32_t* stage = reinterpret_cast<uint32_t*>(smem); // [warp][D / 2]
   if (lane < kPer)
 #pragma unroll
     for (int j = 0; j < 4; ++j) stage[warp * (D / 2) + ch * 4 + j] = top[j];
   __syncthreads();
   for (int i = threadIdx.x; i < D / 2; i += blockDim.x) {
-    __half2 m = stage[i];
-    for (int w = 1; w < kWriteWarps; ++w) m = __hmax2(m, stage[w * (D / 2) + i]);
-    s_abs[i] = *reinterpret_cast<const uint32_t*>(&m);
+    uint32_t m = stage[i];
+    for (int w = 1; w < kWriteWarps; ++w) m = max_abs<BF16>(m, stage[w * (D / 2) + i]);
+    s_abs[i] = m;
   }
   cluster.sync();
   float scale[8], inv[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    __half2 m = __float2half2_rn(0.f);
-    for (int r = 0; r < ctas; ++r) {
-      const uint32_t w = *cluster.map_shared_rank(&s_abs[ch * 4 + j], r);
-      m = __hmax2(m, *reinterpret_cast<const __half2*>(&w));
-    }
-    const float2 f = __half22float2(m);
+    uint32_t m = 0;
+    for (int r = 0; r < ctas; ++r) m = max_abs<BF16>(m, *cluster.map_shared_rank(&s_abs[ch * 4 + j], r));
+    const float2 f = __half22float2(half_pair<BF16>(m));
     scale[2 * j] = f.x > 0.f ? __fdiv_rn(f.x, 127.f) : 1.f;
     scale[2 * j + 1] = f.y > 0.f ? __fdiv_rn(f.y, 127.f) : 1.f;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) inv[i] = __fdiv_rn(1.f, scale[i]);
   if (rank == 0 && threadIdx.x < kPer) {
-    float* dst = (is_v ? d.sV : d.sK) + u * D + ch * 8;
+    float* dst = (IS_V ? d.sV : d.sK) + u * D + ch * 8;
     *reinterpret_cast<float4*>(dst) = make_float4(scale[0], scale[1], scale[2], scale[3]);
     *reinterpret_cast<float4*>(dst + 4) = make_float4(scale[4], scale[5], scale[6], scale[7]);
   }
@@ -172,84 +183,91 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 2)
   // ---- blocks: ceil(n8 / 16) of codes, then the ring
   uint8_t* blk = smem + warp * (D / 16) * kChunk;
   constexpr int kRowsPerWarp = 32 / kPer, kIter = 16 / kRowsPerWarp;
-  const int nb8 = (n8 + 15) / 16, nb = nb8 + s.WR / 16;
-  const int first_ring = n8;
-  const int c0 = is_v ? (ch >> 2) * kChunk + (ch & 3) * 4
-                      : ((ch >> 1) >> 2) * kChunk + ((ch >> 1) & 3) * 4 + (ch & 1) * 2;
-  for (int i = rank * kWriteWarps + warp; i < nb; i += ctas * kWriteWarps) {
-    const bool ring = i >= nb8;
+  const int nb8 = (n8 + 15) / 16;
+  for (int i = rank * kWriteWarps + warp; i < nb8; i += ctas * kWriteWarps) {
     uint4 x[kIter];
-    int tau[kIter];
-    bool there[kIter];
 #pragma unroll
     for (int r = 0; r < kIter; ++r) {
-      tau[r] = r * kRowsPerWarp + lane / kPer;
-      int p;
-      if (ring) {                                      // the newest position that falls on the slot
-        const int slot = (i - nb8) * 16 + tau[r];
-        p = T0 - 1 - ((T0 - 1 - slot) % s.WR + s.WR) % s.WR;
-        there[r] = p >= first_ring;
-      } else {
-        p = i * 16 + tau[r];
-        there[r] = p < n8;
-      }
-      x[r] = there[r] ? load_half8(src + p * ts + ch * 8, bf16) : make_uint4(0, 0, 0, 0);
+      const int p = i * 16 + r * kRowsPerWarp + lane / kPer;
+      x[r] = p < n8 ? row(p) : make_uint4(0, 0, 0, 0);
     }
-    if (!ring) {
 #pragma unroll
-      for (int r = 0; r < kIter; ++r) {
-        const __half2* w = reinterpret_cast<const __half2*>(&x[r]);
-        int code[8];
+    for (int r = 0; r < kIter; ++r) {
+      const int tau = r * kRowsPerWarp + lane / kPer;
+      const __half2 v[4] = {half_pair<BF16>(x[r].x), half_pair<BF16>(x[r].y), half_pair<BF16>(x[r].z),
+                            half_pair<BF16>(x[r].w)};
+      const uint2 code = quantise8(v, scale, inv);
+      if (IS_V) {                                      // v8_offset
+        uint8_t* o = blk + (ch >> 2) * kChunk + (ch & 3) * 4 + ((tau & 7) >> 1) * 16 +
+                     (((tau >> 3) << 1) | (tau & 1));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = __half22float2(w[j]);
-          code[2 * j] = there[r] ? quantise(f.x, scale[2 * j], inv[2 * j]) + kCodeBias : kCodeBias;
-          code[2 * j + 1] = there[r] ? quantise(f.y, scale[2 * j + 1], inv[2 * j + 1]) + kCodeBias : kCodeBias;
-        }
-        if (is_v) {                                    // v8_offset
-          uint8_t* o = blk + c0 + ((tau[r] & 7) >> 1) * 16 + (((tau[r] >> 3) << 1) | (tau[r] & 1));
+        for (int j = 0; j < 8; ++j) o[j * 64] = (uint8_t)((j < 4 ? code.x : code.y) >> 8 * (j & 3));
+      } else {                                         // k8_offset
+        uint8_t* o = blk + ((ch >> 3) + (tau >> 3) * (D / 64)) * kChunk + ((ch >> 1) & 3) * 4 + (ch & 1) * 2 +
+                     (tau & 7) * 64;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j * 64] = (uint8_t)code[j];
-        } else {                                       // k8_offset
-          uint8_t* o = blk + c0 + (tau[r] >> 3) * (D / 64) * kChunk + (tau[r] & 7) * 64;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint16_t*>(o + j * 16) = (uint16_t)(code[2 * j] | code[2 * j + 1] << 8);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < kIter; ++r) {
-        const uint16_t* w = reinterpret_cast<const uint16_t*>(&x[r]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int o = is_v ? v16_offset(D, tau[r], ch * 8 + j) : k16_offset(D, tau[r], ch * 8 + j);
-          *reinterpret_cast<uint16_t*>(blk + (o >> 9) * kChunk + (o & 511)) = w[j];
-        }
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint16_t*>(o + j * 16) = (uint16_t)((j < 2 ? code.x : code.y) >> 16 * (j & 1));
       }
     }
     __syncwarp();
-    uint8_t* dst = ring ? reinterpret_cast<uint8_t*>(is_v ? d.v16 : d.k16) + (u * (s.WR / 16) + (i - nb8)) * 32 * D
-                        : (is_v ? d.v8 : d.k8) + (u * (s.cstride / 16) + i) * 16 * D;
-    for (int r = 0; r < (ring ? D / 16 : D / 32); ++r)
+    uint8_t* dst = (IS_V ? d.v8 : d.k8) + (u * (s.cstride / 16) + i) * 16 * D;
+#pragma unroll
+    for (int r = 0; r < D / 32; ++r)
+      *reinterpret_cast<uint4*>(dst + r * 512 + lane * 16) = *reinterpret_cast<const uint4*>(blk + r * kChunk + lane * 16);
+    __syncwarp();
+  }
+  for (int i = rank * kWriteWarps + warp; i < s.WR / 16; i += ctas * kWriteWarps) {
+#pragma unroll
+    for (int r = 0; r < kIter; ++r) {                  // the newest position that falls on each slot
+      const int tau = r * kRowsPerWarp + lane / kPer;
+      const int p = T0 - 1 - ((T0 - 1 - (i * 16 + tau)) % s.WR + s.WR) % s.WR;
+      const uint4 x = p >= n8 ? row(p) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2 v = half_pair<BF16>((&x.x)[j]);
+        const int o0 = IS_V ? v16_offset(D, tau, ch * 8 + 2 * j) : k16_offset(D, tau, ch * 8 + 2 * j);
+        const int o1 = IS_V ? v16_offset(D, tau, ch * 8 + 2 * j + 1) : o0 + 2;
+        *reinterpret_cast<__half*>(blk + (o0 >> 9) * kChunk + (o0 & 511)) = __low2half(v);
+        *reinterpret_cast<__half*>(blk + (o1 >> 9) * kChunk + (o1 & 511)) = __high2half(v);
+      }
+    }
+    __syncwarp();
+    uint8_t* dst = reinterpret_cast<uint8_t*>(IS_V ? d.v16 : d.k16) + (u * (s.WR / 16) + i) * 32 * D;
+#pragma unroll
+    for (int r = 0; r < D / 16; ++r)
       *reinterpret_cast<uint4*>(dst + r * 512 + lane * 16) = *reinterpret_cast<const uint4*>(blk + r * kChunk + lane * 16);
     __syncwarp();
   }
   // ---- positions and EMA of the layer's slots, by the K of KV head 0
-  if (h == 0 && !is_v) {
+  if (h == 0 && !IS_V) {
     for (int i = rank * blockDim.x + threadIdx.x; i < s.S; i += ctas * blockDim.x) {
       int p = -1;
       if (i < n8) {
         p = i;
-      } else if (i >= s.cap && T0 > 0) {
-        const int slot = i - s.cap, back = ((T0 - 1 - slot) % s.WR + s.WR) % s.WR;
-        p = T0 - 1 - back >= first_ring ? T0 - 1 - back : -1;
+      } else if (i >= s.cap) {
+        const int at = T0 - 1 - ((T0 - 1 - (i - s.cap)) % s.WR + s.WR) % s.WR;
+        p = at >= n8 ? at : -1;
       }
       d.pos[lb * s.S + i] = p;
       d.ema[lb * s.S + i] = 0.f;
     }
     if (rank == 0 && threadIdx.x == 0) d.n8[lb] = n8;
   }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kWriteWarps * 32, 3)
+    write_layer_kernel(Shape s, Dev d, int layer, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
+                       long long k_t, long long k_h, long long v_t, long long v_h) {
+  extern __shared__ __align__(16) uint8_t smem[];      // an interleaved block per warp
+  __shared__ uint32_t s_abs[D / 2];                    // absmax of this CTA's tokens, channel pairs
+  const int unit = blockIdx.x / (int)cg::this_cluster().num_blocks();   // (sequence, KV head, K or V)
+  const int h = (unit >> 1) % s.Hkv, b = (unit >> 1) / s.Hkv;
+  if (unit & 1)
+    write_unit<D, BF16, true>(s, d, layer, b, h, v + d.row0[b] * v_t + h * v_h, v_t, smem, s_abs);
+  else
+    write_unit<D, BF16, false>(s, d, layer, b, h, k + d.row0[b] * k_t + h * k_h, k_t, smem, s_abs);
 }
 
 // ------------------------------------------------------------------ read
@@ -301,24 +319,53 @@ __device__ __forceinline__ uint4 dequantise(uint2 w, const float* scale, bool bf
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kReadWarps * 32)
-    read_layer_kernel(Shape s, Dev d, int layer, int bf16, int spans, const int32_t* __restrict__ cu,
+// Sequences whose entries every CTA of the read kernel counts by itself.
+// Counting in a launch of its own costs about 4 us before the read can start;
+// the CTAs' own counts read B * WR positions each, which for more sequences
+// is more than their blocks.
+constexpr int kCountHere = 16;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kReadWarps * 32, 3)
+    read_layer_kernel(Shape s, Dev d, int layer, int spans, int per_warp, int counted, int32_t* __restrict__ cu,
                       uint16_t* __restrict__ k, uint16_t* __restrict__ v, long long k_t, long long k_h,
                       long long v_t, long long v_h, int32_t* __restrict__ positions, int rows) {
   constexpr int kPer = D / 8, kRowsAtOnce = 32 / kPer, kPitch = D + 16;
   __shared__ __align__(16) uint8_t s_blk[kReadWarps][32 * kPitch];   // 16 rows of bytes, or of halves
+  __shared__ int s_count[kCountHere];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / spans, h = unit % s.Hkv, b = unit / s.Hkv;
-  const int ch = lane % kPer;
+  const int ch = lane % kPer, g = lane >> 2, t = lane & 3;
   pdl_wait();
   const size_t lb = lb_index(s, layer, b), u = unit_index(s, layer, b, h);
+  int row0;
+  if (counted) {
+    row0 = cu[b];
+  } else {
+    for (int i = warp; i < s.B; i += kReadWarps) {
+      const size_t at = lb_index(s, layer, i);
+      int n = 0;
+      for (int j = lane; j < s.WR; j += 32) n += d.pos[at * s.S + s.cap + j] >= 0;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) s_count[i] = n + d.n8[at];
+    }
+    __syncthreads();
+    row0 = 0;
+    for (int i = 0; i < b; ++i) row0 += s_count[i];
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      int sum = 0;
+      for (int i = 0; i < s.B; ++i) {
+        cu[i] = sum;
+        sum += s_count[i];
+      }
+      cu[s.B] = sum;
+    }
+  }
   const int n8 = d.n8[lb], nb8 = (n8 + 15) / 16, nb = nb8 + s.WR / 16;
-  const int row0 = cu[b];
   const int32_t* pos = d.pos + lb * s.S;
   uint8_t* blk = s_blk[warp];
-  const int i0 = ((blockIdx.x % spans) * kReadWarps + warp) * kReadBlocks;
-  for (int i = i0; i < min(i0 + kReadBlocks, nb); ++i) {
+  const int i0 = ((blockIdx.x % spans) * kReadWarps + warp) * per_warp;
+  for (int i = i0; i < min(i0 + per_warp, nb); ++i) {
     const bool ring = i >= nb8;
     // output row of slot `lane` (lanes 0-15); -1: nothing there
     int row = -1, p = -1;
@@ -328,63 +375,81 @@ __global__ void __launch_bounds__(kReadWarps * 32)
         row = row0 + slot;
         p = pos[slot];
       }
-    } else {
+    } else {                                           // by position: behind the older entries of the ring
       const int32_t* rp = pos + s.cap;
       p = lane < 16 ? rp[(i - nb8) * 16 + lane] : -1;
-      int older = 0;
-      for (int j0 = 0; j0 < s.WR; j0 += 32) {
-        const int q = j0 + lane < s.WR ? rp[j0 + lane] : -1;
-        for (int j = 0; j < 32; ++j) {
-          const int x = __shfl_sync(0xffffffffu, q, j);
-          older += x >= 0 && x < p;
-        }
+      int older[16] = {};
+      for (int j = lane; j < s.WR; j += 32) {
+        const int x = rp[j];
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          older[q] += x >= 0 && x < rp[(i - nb8) * 16 + q];
       }
-      if (p >= 0) row = row0 + n8 + older;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int n = __reduce_add_sync(0xffffffffu, older[q]);
+        if (lane == q && p >= 0) row = row0 + n8 + n;
+      }
     }
     if (row >= rows) {
       atomicOr(d.status, kStatusCapacity);
       row = -1;
     }
     if (h == 0 && row >= 0) positions[row] = p;
+    const uint8_t* code[2] = {d.k8 + (u * (s.cstride / 16) + i) * 16 * D, d.v8 + (u * (s.cstride / 16) + i) * 16 * D};
+    uint4 x[2][D / 32];
+    if (!ring) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int r = 0; r < D / 32; ++r) x[kv][r] = *reinterpret_cast<const uint4*>(code[kv] + r * 512 + lane * 16);
+    }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       float scale[8];
       if (!ring) {
-        const uint8_t* src = (kv ? d.v8 : d.k8) + (u * (s.cstride / 16) + i) * 16 * D;
         const float4* sc = reinterpret_cast<const float4*>((kv ? d.sV : d.sK) + u * D + ch * 8);
         const float4 s0 = sc[0], s1 = sc[1];
         scale[0] = s0.x; scale[1] = s0.y; scale[2] = s0.z; scale[3] = s0.w;
         scale[4] = s1.x; scale[5] = s1.y; scale[6] = s1.z; scale[7] = s1.w;
-        const int g = lane >> 2, t = lane & 3;
-        uint4 x[D / 32];
-#pragma unroll
-        for (int r = 0; r < D / 32; ++r) x[r] = *reinterpret_cast<const uint4*>(src + r * 512 + lane * 16);
 #pragma unroll
         for (int r = 0; r < D / 32; ++r) {
-          const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            const uint32_t w = (&x[kv][r].x)[j];
             if (kv) {                                  // v8_offset: channel 8 (4 r + j) + g, four tokens
               uint8_t* o = blk + (4 * r + j) * 8 + g;
-              o[(2 * t) * kPitch] = (uint8_t)w[j];
-              o[(2 * t + 1) * kPitch] = (uint8_t)(w[j] >> 8);
-              o[(2 * t + 8) * kPitch] = (uint8_t)(w[j] >> 16);
-              o[(2 * t + 9) * kPitch] = (uint8_t)(w[j] >> 24);
+              o[(2 * t) * kPitch] = (uint8_t)w;
+              o[(2 * t + 1) * kPitch] = (uint8_t)(w >> 8);
+              o[(2 * t + 8) * kPitch] = (uint8_t)(w >> 16);
+              o[(2 * t + 9) * kPitch] = (uint8_t)(w >> 24);
             } else {                                   // k8_offset: token 8 nt + g, two channel pairs
               const int nt = r / (D / 64), kk = (r % (D / 64)) * 4 + j;
               uint8_t* o = blk + (8 * nt + g) * kPitch + 16 * kk + 2 * t;
-              *reinterpret_cast<uint16_t*>(o) = (uint16_t)w[j];
-              *reinterpret_cast<uint16_t*>(o + 8) = (uint16_t)(w[j] >> 16);
+              *reinterpret_cast<uint16_t*>(o) = (uint16_t)w;
+              *reinterpret_cast<uint16_t*>(o + 8) = (uint16_t)(w >> 16);
             }
           }
         }
       } else {
         const uint8_t* src = reinterpret_cast<const uint8_t*>(kv ? d.v16 : d.k16) +
                              (u * (s.WR / 16) + (i - nb8)) * 32 * D;
-        for (int e = lane; e < 16 * D; e += 32) {
-          const int tau = e / D, c = e % D;
-          const int o = kv ? v16_offset(D, tau, c) : k16_offset(D, tau, c);
-          reinterpret_cast<uint16_t*>(blk)[tau * kPitch + c] = *reinterpret_cast<const uint16_t*>(src + o);
+        uint16_t* half = reinterpret_cast<uint16_t*>(blk);
+#pragma unroll
+        for (int r = 0; r < D / 16; ++r) {
+          const uint4 y = *reinterpret_cast<const uint4*>(src + r * 512 + lane * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = (&y.x)[j];
+            if (kv) {                                  // v16_offset: channel 8 (2 r + j / 2) + g, two tokens
+              const int c = 8 * (2 * r + (j >> 1)) + g, tau = 8 * (j & 1) + 2 * t;
+              half[tau * kPitch + c] = (uint16_t)w;
+              half[(tau + 1) * kPitch + c] = (uint16_t)(w >> 16);
+            } else {                                   // k16_offset: token 8 nt + g, a channel pair
+              const int nt = r / (D / 32), kk = 2 * (r % (D / 32)) + (j >> 1);
+              *reinterpret_cast<uint32_t*>(half + (8 * nt + g) * kPitch + 16 * kk + 8 * (j & 1) + 2 * t) = w;
+            }
+          }
         }
       }
       __syncwarp();
@@ -394,13 +459,12 @@ __global__ void __launch_bounds__(kReadWarps * 32)
       for (int r = 0; r < 16; r += kRowsAtOnce) {
         const int tau = r + lane / kPer;
         const int to = __shfl_sync(0xffffffffu, row, tau);
-        if (to < 0) continue;
         uint4 y;
         if (!ring) {
-          y = dequantise(*reinterpret_cast<const uint2*>(blk + tau * kPitch + ch * 8), scale, bf16);
+          y = dequantise(*reinterpret_cast<const uint2*>(blk + tau * kPitch + ch * 8), scale, BF16);
         } else {
           y = *reinterpret_cast<const uint4*>(blk + (tau * kPitch + ch * 8) * 2);
-          if (bf16) {
+          if (BF16) {
             uint32_t* w = &y.x;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -410,7 +474,7 @@ __global__ void __launch_bounds__(kReadWarps * 32)
             }
           }
         }
-        *reinterpret_cast<uint4*>(out + to * ot) = y;
+        if (to >= 0) *reinterpret_cast<uint4*>(out + to * ot) = y;
       }
       __syncwarp();
     }
@@ -431,14 +495,14 @@ int launch_prefill_reset(const Shape& s, const Dev& d, const int32_t* len, cudaS
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-template <int D>
-static int launch_write(const Shape& s, const Dev& d, int layer, bool bf16, const void* k, const void* v,
-                        const int64_t* ks, const int64_t* vs, int max_len, cudaStream_t st) {
+template <int D, bool BF16>
+static int launch_write(const Shape& s, const Dev& d, int layer, const void* k, const void* v, const int64_t* ks,
+                        const int64_t* vs, int max_len, cudaStream_t st) {
   static int done[kMaxDevices] = {};
   constexpr int smem = kWriteWarps * (D / 16) * kChunk;
-  if (ensure_smem(write_layer_kernel<D>, smem, done) != cudaSuccess) return -1;
-  // CTAs per (sequence, head, K or V): enough to fill the GPU twice, as long
-  // as each still has 64 tokens
+  if (ensure_smem(write_layer_kernel<D, BF16>, smem, done) != cudaSuccess) return -1;
+  // CTAs per (sequence, head, K or V): enough to fill the GPU, as long as
+  // each still has 64 tokens
   const long long units = 2LL * s.B * s.Hkv;
   int ctas = 1;
   while (ctas < 8 && units * ctas < 4LL * 152 && max_len / (2 * ctas) >= 64) ctas *= 2;
@@ -453,26 +517,33 @@ static int launch_write(const Shape& s, const Dev& d, int layer, bool bf16, cons
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, write_layer_kernel<D>, s, d, layer, (int)bf16, static_cast<const uint16_t*>(k),
+  return cudaLaunchKernelEx(&cfg, write_layer_kernel<D, BF16>, s, d, layer, static_cast<const uint16_t*>(k),
                             static_cast<const uint16_t*>(v), (long long)ks[0], (long long)ks[1], (long long)vs[0],
-                            (long long)vs[1]) == cudaSuccess ? 0 : -1;
+                            (long long)vs[1]) == cudaSuccess
+             ? 0
+             : -1;
 }
 
 int launch_write_layer(const Shape& s, const Dev& d, int layer, bool bf16, const void* k, const void* v,
                        const int64_t* k_stride, const int64_t* v_stride, int max_len, cudaStream_t st) {
-  return s.D == 128 ? launch_write<128>(s, d, layer, bf16, k, v, k_stride, v_stride, max_len, st)
-                    : launch_write<64>(s, d, layer, bf16, k, v, k_stride, v_stride, max_len, st);
+  auto fn = s.D == 128 ? (bf16 ? launch_write<128, true> : launch_write<128, false>)
+                       : (bf16 ? launch_write<64, true> : launch_write<64, false>);
+  return fn(s, d, layer, k, v, k_stride, v_stride, max_len, st);
 }
 
 int launch_read_layer(const Shape& s, const Dev& d, int layer, bool bf16, void* k, void* v, const int64_t* ks,
                       const int64_t* vs, int32_t* positions, int32_t* cu, int rows, long long n8_bound,
                       cudaStream_t st) {
-  count_entries_kernel<<<1, 1024, 0, st>>>(s, d, layer, cu);
-  const long long blocks = (n8_bound + 15) / 16 + s.WR / 16;
-  const int spans = (int)((blocks + kReadWarps * kReadBlocks - 1) / (kReadWarps * kReadBlocks));
-  const dim3 grid((unsigned)((long long)spans * s.B * s.Hkv));
-  auto kernel = s.D == 128 ? read_layer_kernel<128> : read_layer_kernel<64>;
-  return launch_pdl(kernel, grid, dim3(kReadWarps * 32), 0, st, s, d, layer, (int)bf16, spans, (const int32_t*)cu,
+  const bool counted = s.B > kCountHere;
+  if (counted) count_entries_kernel<<<1, 1024, 0, st>>>(s, d, layer, cu);
+  // one block per warp until the GPU is full, then up to four
+  const long long blocks = (n8_bound + 15) / 16 + s.WR / 16, units = (long long)s.B * s.Hkv;
+  const long long per_warp = std::min(4LL, std::max(1LL, blocks * units / (152LL * 6 * kReadWarps)));
+  const int spans = (int)((blocks + kReadWarps * per_warp - 1) / (kReadWarps * per_warp));
+  const dim3 grid((unsigned)(spans * units));
+  auto kernel = s.D == 128 ? (bf16 ? read_layer_kernel<128, true> : read_layer_kernel<128, false>)
+                           : (bf16 ? read_layer_kernel<64, true> : read_layer_kernel<64, false>);
+  return launch_pdl(kernel, grid, dim3(kReadWarps * 32), 0, st, s, d, layer, spans, (int)per_warp, (int)counted, cu,
                     static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), (long long)ks[0], (long long)ks[1],
                     (long long)vs[0], (long long)vs[1], positions, rows) == cudaSuccess
              ? 0

@@ -54,26 +54,49 @@ __device__ __forceinline__ void store1(void* p, long long i, int type, float x) 
     static_cast<__half*>(p)[i] = __float2half_rn(x);
 }
 
-// 8 consecutive elements from element offset i (a multiple of 8).
+// 8 consecutive elements as they lie in memory, from element offset i (a
+// multiple of 8), and as fp32.
+template <int TYPE>
+struct Raw {
+  uint4 w[TYPE == CONFKV_FP32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, long long i) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (TYPE == CONFKV_FP32 ? 4 : 2));
+    w[0] = src[0];
+    if (TYPE == CONFKV_FP32) w[TYPE == CONFKV_FP32] = src[1];
+  }
+  __device__ __forceinline__ void floats(float* x) const {
+    const uint32_t* u = &w[0].x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (TYPE == CONFKV_FP32) {
+        x[j] = __uint_as_float(u[j]);
+        x[4 + j] = __uint_as_float((&w[TYPE == CONFKV_FP32].x)[j]);
+      } else if (TYPE == CONFKV_BF16) {
+        x[2 * j] = __uint_as_float(u[j] << 16);
+        x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      }
+    }
+  }
+};
 __device__ __forceinline__ void load8(const void* p, long long i, int type, float* x) {
   if (type == CONFKV_FP32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = f[0], b = f[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    return;
-  }
-  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float2 f;
-    if (type == CONFKV_BF16)
-      f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
-    else
-      f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-    x[2 * j] = f.x;
-    x[2 * j + 1] = f.y;
+    Raw<CONFKV_FP32> r;
+    r.load(p, i);
+    r.floats(x);
+  } else {
+    Raw<CONFKV_FP16> r;
+    r.load(p, i);
+    if (type == CONFKV_FP16) {
+      r.floats(x);
+    } else {
+      Raw<CONFKV_BF16> t;
+      t.w[0] = r.w[0];
+      t.floats(x);
+    }
   }
 }
 __device__ __forceinline__ void store8(void* p, long long i, int type, const float* x) {
@@ -105,24 +128,35 @@ __device__ __forceinline__ void angle(const RotArgs& a, int pos, int i, float* c
 }
 
 // TPR threads per row, two 8-channel chunks each.  Groups of TPR threads
-// take heads slot, slot + slots, ... of their token.
-template <int TPR>
-__global__ void __launch_bounds__(256) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
+// take heads slot, slot + slots, ... of their token, the next head's row in
+// flight while they work on one.
+template <int TPR, int IN>
+__global__ void __launch_bounds__(256, 3) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
   const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
   const int t = (int)(gid % TPR), heads = a.Hq + a.Hkv;
   const long long group = gid / TPR;
   const int token = (int)(group / a.slots), slot = (int)(group % a.slots);
   const bool in = token < a.n;
-  // chunks of this thread and whether they are rotated
+  // chunks of this thread and whether they are rotated (both or neither:
+  // rot is a multiple of 16)
   const int half = a.rot / 16;                 // chunks of one half of the rotated part
   int c0 = 2 * t, c1 = 2 * t + 1;
   if (!a.interleaved && t < half) {
     c0 = t;
     c1 = t + half;
   }
-  const bool r0 = c0 < 2 * half, r1 = c1 < 2 * half;
+  const bool turned = t < half;
+  auto fetch = [&](int head, Raw<IN>& r0, Raw<IN>& r1) {
+    const bool is_q = head < a.Hq;
+    const void* src = is_q ? a.q : a.k;
+    const long long off = is_q ? token * a.q_t + head * a.q_h : token * a.k_t + (head - a.Hq) * a.k_h;
+    r0.load(src, off + 8 * c0);
+    r1.load(src, off + 8 * c1);
+  };
+  Raw<IN> r0 = {}, r1 = {};
+  if (in && slot < heads) fetch(slot, r0, r1);
   float co[8], si[8];
-  if (in && r0) {
+  if (in && turned) {
     const int pos = a.pos[token];
 #pragma unroll
     for (int i = 0; i < 8; ++i) angle(a, pos, 8 * t + i, &co[i], &si[i]);
@@ -132,12 +166,9 @@ __global__ void __launch_bounds__(256) rotary_rows_kernel(const __grid_constant_
     const bool on = in && head < heads;
     const bool is_q = head < a.Hq;
     float x[16];
-    if (on) {
-      const void* src = is_q ? a.q : a.k;
-      const long long off = is_q ? token * a.q_t + head * a.q_h : token * a.k_t + (head - a.Hq) * a.k_h;
-      load8(src, off + 8 * c0, a.in_type, x);
-      load8(src, off + 8 * c1, a.in_type, x + 8);
-    }
+    r0.floats(x);
+    r1.floats(x + 8);
+    if (in && head + a.slots < heads) fetch(head + a.slots, r0, r1);
     const void* weight = is_q ? a.qw : a.kw;
     if (a.qw || a.kw) {
       float ss = 0.f;
@@ -160,13 +191,13 @@ __global__ void __launch_bounds__(256) rotary_rows_kernel(const __grid_constant_
     if (a.interleaved) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i < 4 ? r0 : r1) {
+        if (turned) {
           const float u = x[2 * i], v = x[2 * i + 1];
           x[2 * i] = u * co[i] - v * si[i];
           x[2 * i + 1] = v * co[i] + u * si[i];
         }
       }
-    } else if (r0) {
+    } else if (turned) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float u = x[i], v = x[8 + i];
@@ -252,8 +283,10 @@ bool same_place(const void* p, const int64_t* ps, const void* o, const int64_t* 
 
 template <int TPR>
 void launch_rows(const RotArgs& a, cudaStream_t st) {
-  const long long threads = (long long)a.n * a.slots * TPR;
-  rotary_rows_kernel<TPR><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
+  const unsigned blocks = (unsigned)(((long long)a.n * a.slots * TPR + 255) / 256);
+  if (a.in_type == CONFKV_FP32) rotary_rows_kernel<TPR, CONFKV_FP32><<<blocks, 256, 0, st>>>(a);
+  else if (a.in_type == CONFKV_BF16) rotary_rows_kernel<TPR, CONFKV_BF16><<<blocks, 256, 0, st>>>(a);
+  else rotary_rows_kernel<TPR, CONFKV_FP16><<<blocks, 256, 0, st>>>(a);
 }
 
 }  // namespace
@@ -336,10 +369,10 @@ extern "C" int confkv_qk_rotary(const confkv_rotary_args* p, void* stream) {
                     at(a.qw, 16) && at(a.kw, 16);
   if (rows) {
     const int tpr = p->d / 16;
-    // one head per thread group until the GPU is full, then up to eight
+    // one head per thread group until the GPU is full, then up to four
     const long long full = 152LL * 2048;
     long long per = (long long)p->n * heads * tpr / full;
-    per = per < 1 ? 1 : per > 8 ? 8 : per;
+    per = per < 1 ? 1 : per > 4 ? 4 : per;
     a.slots = (int)((heads + per - 1) / per);
     if ((long long)p->n * a.slots * tpr / 256 + 1 >= (1LL << 31)) return CONFKV_EINVAL;
     if (tpr == 4) launch_rows<4>(a, st);

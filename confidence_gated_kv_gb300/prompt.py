@@ -7,15 +7,24 @@ of a cache are methods of Cache.
 from __future__ import annotations
 
 import ctypes
-import math
 import struct
 
-from .binding import _check, _stream, dtype_code, lib, on_device
+from .binding import FP32, _check, _stream, dtype_code, lib, on_device
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 _ROTARY = struct.Struct("=10i2f4Q8q4Q")
 _PROMPT = struct.Struct("=8if4x7Q8q")
+
+
+def _int32():
+    import torch
+    return torch.int32
+
+
+def _float32():
+    import torch
+    return torch.float32
 
 
 class Rotary:
@@ -30,7 +39,7 @@ class Rotary:
         import torch
         if scaling not in SCALINGS:
             raise ValueError("scaling is one of %s" % ", ".join(SCALINGS))
-        self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
+        self.rot_dim, self.interleaved = int(rot_dim), int(bool(interleaved))
         host = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
         mscale = ctypes.c_float()
         _check(lib().confkv_rotary_frequencies(self.rot_dim, float(base), SCALINGS[scaling], float(factor),
@@ -41,27 +50,39 @@ class Rotary:
         signed = [x - (1 << 64) if x >= 1 << 63 else x for x in self.turns_host]
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.turns = torch.tensor(signed, dtype=torch.int64, device=dev)
+        self.turns_at, self.device_index = self.turns.data_ptr(), self.turns.get_device()
 
 
-def _rows(t, name, heads=None):
-    """Checks a [rows, heads, d] tensor; (rows, heads, d)."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError("%s: a [rows, heads, channels] tensor with contiguous channels is wanted" % name)
-    if not t.is_cuda:
-        raise ValueError("%s: a CUDA tensor is wanted" % name)
-    return t.shape
+def _unfit(what):
+    raise ValueError(what)
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+def _dims(t, name, dev=None):
+    """(rows, heads, d) and strides of a [rows, heads, d] CUDA tensor with
+    contiguous channels, on device `dev` if one is given."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
+        _unfit("%s: a [rows, heads, channels] tensor with contiguous channels is wanted" % name)
+    if not t.is_cuda or (dev is not None and t.get_device() != dev):
+        _unfit("%s: a CUDA tensor%s is wanted, not one on %s"
+               % (name, "" if dev is None else " on the device of q", t.device))
+    return shape, stride
 
 
-def _vector(t, name, n, dtype=None):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or (dtype is not None and t.dtype != dtype):
-        raise ValueError("%s: a contiguous vector of %d%s is wanted"
-                         % (name, n, "" if dtype is None else " " + str(dtype)))
+def _vector(t, name, n, dtype, dev):
+    """Address of a contiguous vector of n elements on device `dev`."""
+    if t.shape != (n,) or (n > 1 and not t.is_contiguous()) or (dtype is not None and t.dtype != dtype):
+        _unfit("%s: a contiguous vector of %d%s is wanted" % (name, n, "" if dtype is None else " " + str(dtype)))
+    if t.get_device() != dev:
+        _unfit("%s is on %s, not on the device of q" % (name, t.device))
+    return t.data_ptr()
+
+
+def _launch(fn, name, args, dev, stream):
+    with on_device(dev):
+        st = fn(args, _stream(stream, dev))
+    if st:
+        _check(st, name)
 
 
 def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
@@ -71,51 +92,46 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
     None (norms only), k None (queries only).  Returns (q_out, k_out): new
     tensors of the inputs' type, or the given ones, which may be of another
     type, strided, or the inputs themselves."""
-    import torch
-    n, Hq, d = _rows(q, "q")
-    Hkv = 0
-    if k is not None:
-        nk, Hkv, dk = _rows(k, "k")
-        if nk != n or dk != d or k.dtype != q.dtype:
-            raise ValueError("k: rows, channels and type of q are wanted")
-    dev = q.device
+    (n, Hq, d), qs = _dims(q, "q")
+    dev, code = q.get_device(), dtype_code(q.dtype)
     if q_out is None:
-        q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
-    elif tuple(_rows(q_out, "q_out")) != (n, Hq, d):
-        raise ValueError("q_out: the shape of q is wanted")
-    if k is not None:
+        q_out, qo_code, qos = q.new_empty((n, Hq, d)), code, (Hq * d, d)
+    else:
+        shape, qos = _dims(q_out, "q_out", dev)
+        qo_code = dtype_code(q_out.dtype)
+        if shape != q.shape:
+            _unfit("q_out: the shape of q is wanted")
+    Hkv, ks, kos, k_at, ko_at, ko_code = 0, (0, 0), (0, 0), 0, 0, 0
+    if k is None:
+        k_out = None
+    else:
+        (nk, Hkv, dk), ks = _dims(k, "k", dev)
+        if nk != n or dk != d or k.dtype != q.dtype:
+            _unfit("k: rows, channels and type of q are wanted")
         if k_out is None:
-            k_out = torch.empty((n, Hkv, d), dtype=k.dtype, device=dev)
-        elif tuple(_rows(k_out, "k_out")) != (n, Hkv, d):
-            raise ValueError("k_out: the shape of k is wanted")
-    w = q_weight if q_weight is not None else k_weight
+            k_out, ko_code, kos = k.new_empty((n, Hkv, d)), code, (Hkv * d, d)
+        else:
+            shape, kos = _dims(k_out, "k_out", dev)
+            ko_code = dtype_code(k_out.dtype)
+            if shape != k.shape:
+                _unfit("k_out: the shape of k is wanted")
+        k_at, ko_at = k.data_ptr(), k_out.data_ptr()
+    qw_at = kw_at = w_code = pos_at = turns_at = rot = interleaved = 0
+    mscale = 1.0
     if q_weight is not None:
-        _vector(q_weight, "q_weight", d)
+        w_code, qw_at = dtype_code(q_weight.dtype), _vector(q_weight, "q_weight", d, None, dev)
     if k_weight is not None:
-        _vector(k_weight, "k_weight", d, w.dtype)
-    rot, interleaved, mscale, turns = 0, 0, 1.0, None
+        kw_at = _vector(k_weight, "k_weight", d, None if q_weight is None else q_weight.dtype, dev)
+        w_code = dtype_code(k_weight.dtype)
     if rotary is not None:
-        rot, interleaved, mscale, turns = rotary.rot_dim, int(rotary.interleaved), rotary.mscale, rotary.turns
-        if positions is None:
-            raise ValueError("positions are wanted with a rotary table")
-        _vector(positions, "positions", n, torch.int32)
-    _same_device(dev, k=k, positions=positions, turns=turns, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
-                 k_out=k_out if k is not None else None)
-
-    def at(t):
-        return 0 if t is None else t.data_ptr()
-
-    def strides(t):
-        return (0, 0) if t is None else t.stride()[:2]
-
-    ko = k_out if k is not None else None
-    args = _ROTARY.pack(n, Hq, Hkv, d, rot, interleaved, dtype_code(q.dtype),
-                        dtype_code(w.dtype) if w is not None else 0, dtype_code(q_out.dtype),
-                        dtype_code(ko.dtype) if ko is not None else 0, eps, mscale, q.data_ptr(), at(k),
-                        q_out.data_ptr(), at(ko), *q.stride()[:2], *strides(k), *q_out.stride()[:2], *strides(ko),
-                        at(q_weight), at(k_weight), at(positions) if rot else 0, at(turns))
-    with on_device(dev):
-        _check(lib().confkv_qk_rotary(args, _stream(stream, dev.index)), "confkv_qk_rotary")
+        rot, interleaved, mscale, turns_at = rotary.rot_dim, rotary.interleaved, rotary.mscale, rotary.turns_at
+        if positions is None or rotary.device_index != dev:
+            _unfit("positions, and a rotary table on the device of q, are wanted")
+        pos_at = _vector(positions, "positions", n, _int32(), dev)
+    args = _ROTARY.pack(n, Hq, Hkv, d, rot, interleaved, code, w_code, qo_code, ko_code, eps, mscale, q.data_ptr(),
+                        k_at, q_out.data_ptr(), ko_at, qs[0], qs[1], ks[0], ks[1], qos[0], qos[1], kos[0], kos[1],
+                        qw_at, kw_at, pos_at, turns_at)
+    _launch(lib().confkv_qk_rotary, "confkv_qk_rotary", args, dev, stream)
     return q_out, k_out
 
 
@@ -127,36 +143,34 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     same for keys (default: cu_seqlens).  With `causal` the queries are the
     last of their sequence's keys.  scale defaults to 1 / sqrt(d).  Returns
     out, or (out, lse) with return_lse; lse is fp32 [rows, Hq]."""
-    import torch
-    nq, Hq, d = _rows(q, "q")
-    nk, Hkv, dk = _rows(k, "k")
-    if tuple(_rows(v, "v")) != (nk, Hkv, dk) or dk != d:
-        raise ValueError("k and v: one shape, and the channels of q, are wanted")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("q, k and v: one type is wanted")
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens
-    B = cu_seqlens.shape[0] - 1
-    _vector(cu_seqlens, "cu_seqlens", B + 1, torch.int32)
-    _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, torch.int32)
-    dev = q.device
+    (nq, Hq, d), qs = _dims(q, "q")
+    dev, dtype = q.get_device(), q.dtype
+    (nk, Hkv, dk), ks = _dims(k, "k", dev)
+    shape, vs = _dims(v, "v", dev)
+    if shape != k.shape or dk != d or k.dtype != dtype or v.dtype != dtype:
+        _unfit("k and v: one shape, and the channels and type of q, are wanted")
+    B = len(cu_seqlens) - 1
+    cu_at = cuk_at = _vector(cu_seqlens, "cu_seqlens", B + 1, _int32(), dev)
+    if cu_seqlens_k is not None:
+        cuk_at = _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, _int32(), dev)
     if out is None:
-        out = torch.empty((nq, Hq, d), dtype=q.dtype, device=dev)
-    elif tuple(_rows(out, "out")) != (nq, Hq, d) or out.dtype != q.dtype:
-        raise ValueError("out: the shape and type of q are wanted")
-    if lse is None:
-        if return_lse:
-            lse = torch.empty((nq, Hq), dtype=torch.float32, device=dev)
-    elif tuple(lse.shape) != (nq, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse: a contiguous fp32 [rows, heads] tensor is wanted")
-    _same_device(dev, k=k, v=v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k, out=out, lse=lse)
-    args = _PROMPT.pack(B, Hq, Hkv, d, dtype_code(q.dtype), int(causal), nq, nk,
-                        1.0 / math.sqrt(d) if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                        out.data_ptr(), 0 if lse is None else lse.data_ptr(), cu_seqlens.data_ptr(),
-                        cu_seqlens_k.data_ptr(), *q.stride()[:2], *k.stride()[:2], *v.stride()[:2],
-                        *out.stride()[:2])
-    with on_device(dev):
-        _check(lib().confkv_prompt_attention(args, _stream(stream, dev.index)), "confkv_prompt_attention")
+        out, os = q.new_empty((nq, Hq, d)), (Hq * d, d)
+    else:
+        shape, os = _dims(out, "out", dev)
+        if shape != q.shape or out.dtype != dtype:
+            _unfit("out: the shape and type of q are wanted")
+    lse_at = 0
+    if lse is not None:
+        if lse.shape != (nq, Hq) or dtype_code(lse.dtype) != FP32 or not lse.is_contiguous() or lse.get_device() != dev:
+            _unfit("lse: a contiguous fp32 [rows, heads] tensor on the device of q is wanted")
+        lse_at = lse.data_ptr()
+    elif return_lse:
+        lse = q.new_empty((nq, Hq), dtype=_float32())
+        lse_at = lse.data_ptr()
+    args = _PROMPT.pack(B, Hq, Hkv, d, dtype_code(dtype), 1 if causal else 0, nq, nk,
+                        d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                        out.data_ptr(), lse_at, cu_at, cuk_at, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1])
+    _launch(lib().confkv_prompt_attention, "confkv_prompt_attention", args, dev, stream)
     return (out, lse) if return_lse else out
 
 
