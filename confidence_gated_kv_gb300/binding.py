@@ -350,11 +350,11 @@ class Cache:
         and type.  Sequence b has rows cu_seqlens[b] to cu_seqlens[b + 1]."""
         import torch
         if out is None:
-            rows, ws = self.read_rows(), self.workspace
-            shape, dt = (rows, self.Hkv, self.d), torch.float16 if dtype is None else dtype
-            k, v = ws.new_empty(shape, dtype=dt), ws.new_empty(shape, dtype=dt)
-            pos = ws.new_empty((rows,), dtype=torch.int32)
-            cu = ws.new_empty((self.B + 1,), dtype=torch.int32)
+            rows, dev = self.read_rows(), self.device
+            k = torch.empty((rows, self.Hkv, self.d), dtype=torch.float16 if dtype is None else dtype, device=dev)
+            v = torch.empty_like(k)
+            pos = torch.empty(rows, dtype=torch.int32, device=dev)
+            cu = torch.empty(self.B + 1, dtype=torch.int32, device=dev)
             out = {"k": k, "v": v, "positions": pos, "cu_seqlens": cu}
             k_at, v_at, ks = k.data_ptr(), v.data_ptr(), _PAIR.pack(self.Hkv * self.d, self.d)
             vs = ks

@@ -28,8 +28,9 @@ namespace cg = cooperative_groups;
 namespace confkv {
 namespace {
 
-constexpr int kChunk = 528;          // shared-memory pitch of a 512-byte piece of an interleaved block
+constexpr int kChunk = 544;          // shared-memory pitch of a 512-byte piece of an interleaved block
 constexpr int kWriteWarps = 8;
+constexpr int kMaxCtas = 8;           // CTAs per cluster of the write
 constexpr int kReadWarps = 8;
 
 // ------------------------------------------------------------------ reset
@@ -79,19 +80,20 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t top, uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// Stored bytes of 8 values: clamp(rint(x / s), -127, 127) + 128, with the
-// IEEE quotient.  x * (1 / s) is within 2 ulp of it (2^-15 up to 127), so the
-// integers agree unless the product lies that close to a half; only then, or
-// for a NaN, are the quotients computed.  Adding 1.5 2^23 + 128 rounds to an
-// integer (ties to even) and leaves the stored byte in the low bits.  No
-// clamp: |x| <= 127 s (1 + 2^-23).
-__device__ __forceinline__ uint2 quantise8(const __half2 (&x)[4], const float (&scale)[8], const float (&inv)[8]) {
+// 8 values as words whose low byte is clamp(rint(x / s), -127, 127) + 128,
+// with the IEEE quotient.  x * (1 / s) is within 2 ulp of it (2^-15 up to
+// 127), so the integers agree unless the product lies that close to a half;
+// only then, or for a NaN, are the quotients computed.  Adding 1.5 2^23 + 128
+// rounds to an integer (ties to even) and leaves the stored byte in the low
+// bits.  No clamp: |x| <= 127 s (1 + 2^-23).
+template <bool BF16>
+__device__ __forceinline__ void quantise8(const uint4& raw, const float (&scale)[8], const float (&inv)[8],
+                                          uint32_t (&r)[8]) {
   constexpr float kRound = 12582912.f + 128.f;
-  uint32_t r[8];
   bool near = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = __half22float2(x[j]);
+    const float2 f = __half22float2(half_pair<BF16>((&raw.x)[j]));
     const float q0 = f.x * inv[2 * j], q1 = f.y * inv[2 * j + 1];
     const float r0 = q0 + kRound, r1 = q1 + kRound;
     near = near || !(fabsf(q0 - (r0 - kRound)) <= 0.49993f) || !(fabsf(q1 - (r1 - kRound)) <= 0.49993f);
@@ -101,15 +103,11 @@ __device__ __forceinline__ uint2 quantise8(const __half2 (&x)[4], const float (&
   if (near) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(x[j]);
+      const float2 f = __half22float2(half_pair<BF16>((&raw.x)[j]));
       r[2 * j] = (int)fminf(fmaxf(rintf(__fdiv_rn(f.x, scale[2 * j])), -127.f), 127.f) + kCodeBias;
       r[2 * j + 1] = (int)fminf(fmaxf(rintf(__fdiv_rn(f.y, scale[2 * j + 1])), -127.f), 127.f) + kCodeBias;
     }
   }
-  uint2 o;
-  o.x = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
-  o.y = __byte_perm(__byte_perm(r[4], r[5], 0x0040), __byte_perm(r[6], r[7], 0x0040), 0x5410);
-  return o;
 }
 
 template <int D, bool BF16, bool IS_V>
@@ -166,7 +164,9 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t m = 0;
-    for (int r = 0; r < ctas; ++r) m = max_abs<BF16>(m, *cluster.map_shared_rank(&s_abs[ch * 4 + j], r));
+#pragma unroll
+    for (int r = 0; r < kMaxCtas; ++r)
+      if (r < ctas) m = max_abs<BF16>(m, *cluster.map_shared_rank(&s_abs[ch * 4 + j], r));
     const float2 f = __half22float2(half_pair<BF16>(m));
     scale[2 * j] = f.x > 0.f ? __fdiv_rn(f.x, 127.f) : 1.f;
     scale[2 * j + 1] = f.y > 0.f ? __fdiv_rn(f.y, 127.f) : 1.f;
@@ -182,32 +182,40 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
 
   // ---- blocks: ceil(n8 / 16) of codes, then the ring
   uint8_t* blk = smem + warp * (D / 16) * kChunk;
-  constexpr int kRowsPerWarp = 32 / kPer, kIter = 16 / kRowsPerWarp;
-  const int nb8 = (n8 + 15) / 16;
-  for (int i = rank * kWriteWarps + warp; i < nb8; i += ctas * kWriteWarps) {
+  // A lane takes tokens 2t, 2t + 1, 2t + 8 and 2t + 9 of its channels: the
+  // four bytes of a V word (v8_offset).
+  constexpr int kRowsPerWarp = 32 / kPer, kIter = 16 / kRowsPerWarp, kQuads = kIter / 4;
+  auto token = [&](int r) { return 2 * (lane / kPer + kRowsPerWarp * (r >> 2)) + (r & 1) + 4 * (r & 2); };
+  const int nb8 = (n8 + 15) / 16, step = ctas * kWriteWarps;
+  int i = rank * kWriteWarps + warp;
+  for (; i < nb8; i += step) {
     uint4 x[kIter];
 #pragma unroll
     for (int r = 0; r < kIter; ++r) {
-      const int p = i * 16 + r * kRowsPerWarp + lane / kPer;
+      const int p = i * 16 + token(r);
       x[r] = p < n8 ? row(p) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int r = 0; r < kIter; ++r) {
-      const int tau = r * kRowsPerWarp + lane / kPer;
-      const __half2 v[4] = {half_pair<BF16>(x[r].x), half_pair<BF16>(x[r].y), half_pair<BF16>(x[r].z),
-                            half_pair<BF16>(x[r].w)};
-      const uint2 code = quantise8(v, scale, inv);
-      if (IS_V) {                                      // v8_offset
-        uint8_t* o = blk + (ch >> 2) * kChunk + (ch & 3) * 4 + ((tau & 7) >> 1) * 16 +
-                     (((tau >> 3) << 1) | (tau & 1));
+    for (int quad = 0; quad < kQuads; ++quad) {
+      uint32_t r[4][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j * 64] = (uint8_t)((j < 4 ? code.x : code.y) >> 8 * (j & 3));
+      for (int j = 0; j < 4; ++j) quantise8<BF16>(x[quad * 4 + j], scale, inv, r[j]);
+      if (IS_V) {
+        uint8_t* o = blk + (ch >> 2) * kChunk + (ch & 3) * 4 + (lane / kPer + kRowsPerWarp * quad) * 16;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint32_t*>(o + c * 64) = __byte_perm(__byte_perm(r[0][c], r[1][c], 0x0040),
+                                                                 __byte_perm(r[2][c], r[3][c], 0x0040), 0x5410);
       } else {                                         // k8_offset
-        uint8_t* o = blk + ((ch >> 3) + (tau >> 3) * (D / 64)) * kChunk + ((ch >> 1) & 3) * 4 + (ch & 1) * 2 +
-                     (tau & 7) * 64;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint16_t*>(o + j * 16) = (uint16_t)((j < 2 ? code.x : code.y) >> 16 * (j & 1));
+        for (int j = 0; j < 4; ++j) {
+          const int tau = token(quad * 4 + j);
+          uint8_t* o = blk + ((ch >> 3) + (tau >> 3) * (D / 64)) * kChunk + ((ch >> 1) & 3) * 4 + (ch & 1) * 2 +
+                       (tau & 7) * 64;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint16_t*>(o + c * 16) = (uint16_t)__byte_perm(r[j][2 * c], r[j][2 * c + 1], 0x0040);
+        }
       }
     }
     __syncwarp();
@@ -217,10 +225,10 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
       *reinterpret_cast<uint4*>(dst + r * 512 + lane * 16) = *reinterpret_cast<const uint4*>(blk + r * kChunk + lane * 16);
     __syncwarp();
   }
-  for (int i = rank * kWriteWarps + warp; i < s.WR / 16; i += ctas * kWriteWarps) {
+  for (i -= nb8; i < s.WR / 16; i += step) {
 #pragma unroll
     for (int r = 0; r < kIter; ++r) {                  // the newest position that falls on each slot
-      const int tau = r * kRowsPerWarp + lane / kPer;
+      const int tau = token(r);
       const int p = T0 - 1 - ((T0 - 1 - (i * 16 + tau)) % s.WR + s.WR) % s.WR;
       const uint4 x = p >= n8 ? row(p) : make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -262,6 +270,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 3)
                        long long k_t, long long k_h, long long v_t, long long v_h) {
   extern __shared__ __align__(16) uint8_t smem[];      // an interleaved block per warp
   __shared__ uint32_t s_abs[D / 2];                    // absmax of this CTA's tokens, channel pairs
+  pdl_wait();
   const int unit = blockIdx.x / (int)cg::this_cluster().num_blocks();   // (sequence, KV head, K or V)
   const int h = (unit >> 1) % s.Hkv, b = (unit >> 1) / s.Hkv;
   if (unit & 1)
@@ -505,18 +514,20 @@ static int launch_write(const Shape& s, const Dev& d, int layer, const void* k, 
   // each still has 64 tokens
   const long long units = 2LL * s.B * s.Hkv;
   int ctas = 1;
-  while (ctas < 8 && units * ctas < 4LL * 152 && max_len / (2 * ctas) >= 64) ctas *= 2;
+  while (ctas < kMaxCtas && units * ctas < 4LL * 152 && max_len / (2 * ctas) >= 64) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * ctas));
   cfg.blockDim = dim3(kWriteWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, write_layer_kernel<D, BF16>, s, d, layer, static_cast<const uint16_t*>(k),
                             static_cast<const uint16_t*>(v), (long long)ks[0], (long long)ks[1], (long long)vs[0],
                             (long long)vs[1]) == cudaSuccess

@@ -22,9 +22,9 @@ def _int32():
     return torch.int32
 
 
-def _float32():
+def _new(shape, device):
     import torch
-    return torch.float32
+    return torch.empty(shape, dtype=torch.float32, device=device)
 
 
 class Rotary:
@@ -78,6 +78,12 @@ def _vector(t, name, n, dtype, dev):
     return t.data_ptr()
 
 
+def _like(t):
+    """New contiguous tensor of the shape, type and device of t."""
+    import torch
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _launch(fn, name, args, dev, stream):
     with on_device(dev):
         st = fn(args, _stream(stream, dev))
@@ -95,7 +101,7 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
     (n, Hq, d), qs = _dims(q, "q")
     dev, code = q.get_device(), dtype_code(q.dtype)
     if q_out is None:
-        q_out, qo_code, qos = q.new_empty((n, Hq, d)), code, (Hq * d, d)
+        q_out, qo_code, qos = _like(q), code, (Hq * d, d)
     else:
         shape, qos = _dims(q_out, "q_out", dev)
         qo_code = dtype_code(q_out.dtype)
@@ -109,7 +115,7 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
         if nk != n or dk != d or k.dtype != q.dtype:
             _unfit("k: rows, channels and type of q are wanted")
         if k_out is None:
-            k_out, ko_code, kos = k.new_empty((n, Hkv, d)), code, (Hkv * d, d)
+            k_out, ko_code, kos = _like(k), code, (Hkv * d, d)
         else:
             shape, kos = _dims(k_out, "k_out", dev)
             ko_code = dtype_code(k_out.dtype)
@@ -154,7 +160,7 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     if cu_seqlens_k is not None:
         cuk_at = _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, _int32(), dev)
     if out is None:
-        out, os = q.new_empty((nq, Hq, d)), (Hq * d, d)
+        out, os = _like(q), (Hq * d, d)
     else:
         shape, os = _dims(out, "out", dev)
         if shape != q.shape or out.dtype != dtype:
@@ -165,7 +171,7 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
             _unfit("lse: a contiguous fp32 [rows, heads] tensor on the device of q is wanted")
         lse_at = lse.data_ptr()
     elif return_lse:
-        lse = q.new_empty((nq, Hq), dtype=_float32())
+        lse = _new((nq, Hq), q.device)
         lse_at = lse.data_ptr()
     args = _PROMPT.pack(B, Hq, Hkv, d, dtype_code(dtype), 1 if causal else 0, nq, nk,
                         d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
