@@ -86,6 +86,9 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t top, uint32_t w) {
 // only then, or for a NaN, are the quotients computed.  Adding 1.5 2^23 + 128
 // rounds to an integer (ties to even) and leaves the stored byte in the low
 // bits.  No clamp: |x| <= 127 s (1 + 2^-23).
+__device__ __noinline__ uint32_t exact_code(float x, float s) {
+  return (uint32_t)((int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f) + kCodeBias);
+}
 template <bool BF16>
 __device__ __forceinline__ void quantise8(const uint4& raw, const float (&scale)[8], const float (&inv)[8],
                                           uint32_t (&r)[8]) {
@@ -104,8 +107,8 @@ __device__ __forceinline__ void quantise8(const uint4& raw, const float (&scale)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = __half22float2(half_pair<BF16>((&raw.x)[j]));
-      r[2 * j] = (int)fminf(fmaxf(rintf(__fdiv_rn(f.x, scale[2 * j])), -127.f), 127.f) + kCodeBias;
-      r[2 * j + 1] = (int)fminf(fmaxf(rintf(__fdiv_rn(f.y, scale[2 * j + 1])), -127.f), 127.f) + kCodeBias;
+      r[2 * j] = exact_code(f.x, scale[2 * j]);
+      r[2 * j + 1] = exact_code(f.y, scale[2 * j + 1]);
     }
   }
 }
@@ -189,17 +192,17 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
   const int nb8 = (n8 + 15) / 16, step = ctas * kWriteWarps;
   int i = rank * kWriteWarps + warp;
   for (; i < nb8; i += step) {
-    uint4 x[kIter];
-#pragma unroll
-    for (int r = 0; r < kIter; ++r) {
-      const int p = i * 16 + token(r);
-      x[r] = p < n8 ? row(p) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
+#pragma unroll 1
     for (int quad = 0; quad < kQuads; ++quad) {
+      uint4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = i * 16 + token(quad * 4 + j);
+        x[j] = p < n8 ? row(p) : make_uint4(0, 0, 0, 0);
+      }
       uint32_t r[4][8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) quantise8<BF16>(x[quad * 4 + j], scale, inv, r[j]);
+      for (int j = 0; j < 4; ++j) quantise8<BF16>(x[j], scale, inv, r[j]);
       if (IS_V) {
         uint8_t* o = blk + (ch >> 2) * kChunk + (ch & 3) * 4 + (lane / kPer + kRowsPerWarp * quad) * 16;
 #pragma unroll
@@ -265,7 +268,7 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kWriteWarps * 32, 3)
+__global__ void __launch_bounds__(kWriteWarps * 32, 4)
     write_layer_kernel(Shape s, Dev d, int layer, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                        long long k_t, long long k_h, long long v_t, long long v_h) {
   extern __shared__ __align__(16) uint8_t smem[];      // an interleaved block per warp
@@ -335,7 +338,7 @@ __device__ __forceinline__ uint4 dequantise(uint2 w, const float* scale, bool bf
 constexpr int kCountHere = 16;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kReadWarps * 32, 3)
+__global__ void __launch_bounds__(kReadWarps * 32, 4)
     read_layer_kernel(Shape s, Dev d, int layer, int spans, int per_warp, int counted, int32_t* __restrict__ cu,
                       uint16_t* __restrict__ k, uint16_t* __restrict__ v, long long k_t, long long k_h,
                       long long v_t, long long v_h, int32_t* __restrict__ positions, int rows) {
@@ -406,13 +409,6 @@ __global__ void __launch_bounds__(kReadWarps * 32, 3)
     }
     if (h == 0 && row >= 0) positions[row] = p;
     const uint8_t* code[2] = {d.k8 + (u * (s.cstride / 16) + i) * 16 * D, d.v8 + (u * (s.cstride / 16) + i) * 16 * D};
-    uint4 x[2][D / 32];
-    if (!ring) {
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-        for (int r = 0; r < D / 32; ++r) x[kv][r] = *reinterpret_cast<const uint4*>(code[kv] + r * 512 + lane * 16);
-    }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       float scale[8];
@@ -421,11 +417,14 @@ __global__ void __launch_bounds__(kReadWarps * 32, 3)
         const float4 s0 = sc[0], s1 = sc[1];
         scale[0] = s0.x; scale[1] = s0.y; scale[2] = s0.z; scale[3] = s0.w;
         scale[4] = s1.x; scale[5] = s1.y; scale[6] = s1.z; scale[7] = s1.w;
+        uint4 x[D / 32];
+#pragma unroll
+        for (int r = 0; r < D / 32; ++r) x[r] = *reinterpret_cast<const uint4*>(code[kv] + r * 512 + lane * 16);
 #pragma unroll
         for (int r = 0; r < D / 32; ++r) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t w = (&x[kv][r].x)[j];
+            const uint32_t w = (&x[r].x)[j];
             if (kv) {                                  // v8_offset: channel 8 (4 r + j) + g, four tokens
               uint8_t* o = blk + (4 * r + j) * 8 + g;
               o[(2 * t) * kPitch] = (uint8_t)w;
