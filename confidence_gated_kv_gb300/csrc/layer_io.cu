@@ -22,6 +22,7 @@
 
 #include "../../include/confkv.h"
 #include "confkv_internal.cuh"
+#include "fp32_pair.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -93,23 +94,29 @@ template <bool BF16>
 __device__ __forceinline__ void quantise8(const uint4& raw, const float (&scale)[8], const float (&inv)[8],
                                           uint32_t (&r)[8]) {
   constexpr float kRound = 12582912.f + 128.f;
+  float x[8], q[8];
   bool near = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = __half22float2(half_pair<BF16>((&raw.x)[j]));
-    const float q0 = f.x * inv[2 * j], q1 = f.y * inv[2 * j + 1];
-    const float r0 = q0 + kRound, r1 = q1 + kRound;
-    near = near || !(fabsf(q0 - (r0 - kRound)) <= 0.49993f) || !(fabsf(q1 - (r1 - kRound)) <= 0.49993f);
-    r[2 * j] = __float_as_uint(r0);
-    r[2 * j + 1] = __float_as_uint(r1);
+    x[2 * j] = f.x;
+    x[2 * j + 1] = f.y;
   }
-  if (near) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(half_pair<BF16>((&raw.x)[j]));
-      r[2 * j] = exact_code(f.x, scale[2 * j]);
-      r[2 * j + 1] = exact_code(f.y, scale[2 * j + 1]);
-    }
+  for (int j = 0; j < 8; j += 2) {
+    const Pair p = Pair(x[j], x[j + 1]) * Pair(inv[j], inv[j + 1]), whole = p + Pair(kRound, kRound);
+    const Pair off = fma2(whole + Pair(-kRound, -kRound), Pair(-1.f, -1.f), p);
+    near |= !(fabsf(off.get().x) <= 0.49993f);
+    near |= !(fabsf(off.get().y) <= 0.49993f);
+    q[j] = p.get().x;
+    q[j + 1] = p.get().y;
+    r[j] = __float_as_uint(whole.get().x);
+    r[j + 1] = __float_as_uint(whole.get().y);
+  }
+  if (near) {                                          // only the values that are near: a tie is not rare for
+#pragma unroll                                         // a channel whose absmax is a power of two
+    for (int j = 0; j < 8; ++j)
+      if (!(fabsf(q[j] - (__uint_as_float(r[j]) - kRound)) <= 0.49993f)) r[j] = exact_code(x[j], scale[j]);
   }
 }
 
@@ -124,6 +131,7 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
   const int T0 = d.T0[b], n8 = max(0, T0 - s.W);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ch = threadIdx.x % kPer;                   // 8-channel chunk of this thread
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");   // this CTA's shared memory is there
   const size_t lb = lb_index(s, layer, b), u = unit_index(s, layer, b, h);
   auto row = [&](long long t) { return *reinterpret_cast<const uint4*>(src + t * ts + ch * 8); };
 
@@ -157,19 +165,22 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
 #pragma unroll
     for (int j = 0; j < 4; ++j) stage[warp * (D / 2) + ch * 4 + j] = top[j];
   __syncthreads();
-  for (int i = threadIdx.x; i < D / 2; i += blockDim.x) {
-    uint32_t m = stage[i];
-    for (int w = 1; w < kWriteWarps; ++w) m = max_abs<BF16>(m, stage[w * (D / 2) + i]);
-    s_abs[i] = m;
+  asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+  // every CTA sends its maxima to all of the cluster before the one barrier,
+  // so that each reads them locally and may leave when it is done
+  for (int i = threadIdx.x; i < ctas * (D / 2); i += blockDim.x) {
+    const int c = i % (D / 2), to = i / (D / 2);
+    uint32_t m = stage[c];
+#pragma unroll
+    for (int w = 1; w < kWriteWarps; ++w) m = max_abs<BF16>(m, stage[w * (D / 2) + c]);
+    *cluster.map_shared_rank(&s_abs[rank * (D / 2) + c], to) = m;
   }
   cluster.sync();
   float scale[8], inv[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t m = 0;
-#pragma unroll
-    for (int r = 0; r < kMaxCtas; ++r)
-      if (r < ctas) m = max_abs<BF16>(m, *cluster.map_shared_rank(&s_abs[ch * 4 + j], r));
+    for (int r = 0; r < ctas; ++r) m = max_abs<BF16>(m, s_abs[r * (D / 2) + ch * 4 + j]);
     const float2 f = __half22float2(half_pair<BF16>(m));
     scale[2 * j] = f.x > 0.f ? __fdiv_rn(f.x, 127.f) : 1.f;
     scale[2 * j + 1] = f.y > 0.f ? __fdiv_rn(f.y, 127.f) : 1.f;
@@ -181,7 +192,6 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
     *reinterpret_cast<float4*>(dst) = make_float4(scale[0], scale[1], scale[2], scale[3]);
     *reinterpret_cast<float4*>(dst + 4) = make_float4(scale[4], scale[5], scale[6], scale[7]);
   }
-  cluster.sync();                                      // no CTA leaves while another reads its maxima
 
   // ---- blocks: ceil(n8 / 16) of codes, then the ring
   uint8_t* blk = smem + warp * (D / 16) * kChunk;
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 4)
     write_layer_kernel(Shape s, Dev d, int layer, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                        long long k_t, long long k_h, long long v_t, long long v_h) {
   extern __shared__ __align__(16) uint8_t smem[];      // an interleaved block per warp
-  __shared__ uint32_t s_abs[D / 2];                    // absmax of this CTA's tokens, channel pairs
+  __shared__ uint32_t s_abs[kMaxCtas * (D / 2)];       // absmax of each CTA's tokens, channel pairs
   pdl_wait();
   const int unit = blockIdx.x / (int)cg::this_cluster().num_blocks();   // (sequence, KV head, K or V)
   const int h = (unit >> 1) % s.Hkv, b = (unit >> 1) / s.Hkv;

@@ -16,6 +16,7 @@
 
 #include "../../include/confkv.h"
 #include "confkv_internal.cuh"
+#include "fp32_pair.cuh"
 #include "tcgen05.cuh"
 
 namespace confkv {
@@ -366,19 +367,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (move) ref = top;
         const float base = ref == -INFINITY ? 0.f : -ref * a.scale2;
-        const uint64_t scale_pair = pair(a.scale2, a.scale2), base_pair = pair(base, base);
-        uint64_t sum[2] = {0, 0};
+        const Pair scale_pair(a.scale2, a.scale2), base_pair(base, base);
+        Pair sum[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) {           // a quarter of the weights at a time
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float x, y;
-            unpair(fma2(pair(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), scale_pair, base_pair),
-                   x, y);
-            x = ex2(x);
-            y = ex2(y);
-            sum[i & 1] = add2(sum[i & 1], pair(x, y));
+            const float2 e =
+                fma2(Pair(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), scale_pair, base_pair).get();
+            const float x = ex2(e.x), y = ex2(e.y);
+            sum[i & 1] = sum[i & 1] + Pair(x, y);
             p[i] = pack2<BF16>(x, y);
           }
           tmem_st16(ts + c / 2, p);
@@ -388,9 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_arrive(p_full(w, c / 64));
           }
         }
-        float l0, l1;
-        unpair(add2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
+        const float2 both = (sum[0] + sum[1]).get();
+        l += both.x + both.y;
       }
       if (ok && nw > 0) {
         ok = __all_sync(0xffffffffu, wait(o_full(w), 0));

@@ -24,6 +24,7 @@
 
 #include "../../include/confkv.h"
 #include "confkv_internal.cuh"
+#include "fp32_pair.cuh"
 
 namespace confkv {
 namespace {
@@ -126,28 +127,6 @@ __device__ __forceinline__ void angle(const RotArgs& a, int pos, int i, float* c
   sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, s, c);   // 2^-31: half turns
   *c *= a.mscale;
   *s *= a.mscale;
-}
-
-// Pairs of fp32 values in one instruction.
-struct Pair {
-  uint64_t v;
-  __device__ __forceinline__ Pair() {}
-  __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};\n" : "=l"(v) : "f"(lo), "f"(hi)); }
-  __device__ __forceinline__ float2 get() const {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-  }
-};
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
 }
 
 // A block takes `tokens` tokens and `heads` of their heads: it computes the
