@@ -4,12 +4,21 @@
 //   out_i = sum_j softmax_j(scale q_i . k_j) v_j     over the j that row i sees
 //   lse_i = log sum_j exp(scale q_i . k_j)
 //
-// One CTA takes one KV head and two tiles of 128 score rows.  The rows of a
+// A work item is one KV head and two tiles of 128 score rows.  The rows of a
 // tile are (token, query head of the group): all G heads of 128 / G
 // consecutive tokens, so that K and V are read once for the whole group and
 // one token of a decode step still shares one tile.  K and V stream through
 // a ring of shared-memory tiles of 128 keys.
+//
+// Roles of a CTA's 12 warps: a softmax warpgroup per row tile (a thread per
+// row), a warp per row tile that issues the products, one for the copies and
+// one that finds the next item.  A CTA takes over the items of CTAs that have
+// not started (the copies of the next item run behind the last tiles of the
+// current one); with few items the keys of an item are split over a cluster
+// of CTAs instead, which merge their parts through distributed shared memory.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -18,6 +27,8 @@
 #include "confkv_internal.cuh"
 #include "fp32_pair.cuh"
 #include "tcgen05.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace confkv {
 namespace {
@@ -29,15 +40,23 @@ constexpr int kKeys = 128;               // keys per tile
 constexpr int kThreads = 384;            // two softmax warpgroups, one for copies and products
 constexpr int kPolls = 1 << 24;          // polls per wait (a few seconds at most)
 
-template <int D>
+constexpr int kRegs = 168;               // registers a thread at launch: 65536 / 384, in eights
+constexpr int kMaxSplit = 8;             // CTAs of a cluster that share an item
+
+template <int D, bool SPLIT>
 struct Tile {
   static constexpr int kBytes = kRows * D * 2;         // a Q, K or V tile
-  static constexpr int kStages = D == 128 ? 5 : 8;     // K and V tiles in flight
-  static constexpr int kSmem = (2 + kStages) * kBytes + 1024;
+  // K and V tiles in flight; a split item needs room for the merge
+  static constexpr int kStages = (D == 128 ? 5 : 8) - (SPLIT ? 1 : 0);
+  static constexpr int kMerge = SPLIT ? kMaxSplit * 2 * kRows * 8 : 0;
+  static constexpr int kSmem = (2 + kStages) * kBytes + kMerge + 1024;
+  static constexpr int kPitch = D + 4;                 // floats per row of a part
+  static_assert(!SPLIT || 2 * kRows * kPitch * 4 <= (2 + kStages) * kBytes, "a part fits the tiles' place");
 };
 
 struct Args {
   int B, Hq, Hkv, G, tokens;             // tokens: per 128-row tile
+  int split;                             // CTAs per item
   int causal;
   int total_q, total_k;
   const int32_t* cu_q;
@@ -46,20 +65,24 @@ struct Args {
   long long out_token, out_head;
   float* lse;
   float scale, scale2;                   // scale2 = scale * log2(e)
+  int wide;                              // rows of out start on 32-byte boundaries
   int32_t* status;
 };
 
 struct Item {                            // what one CTA computes
+  int found;                             // 0: no more work
   int q0, lq, k0, lk;                    // packed rows and lengths of the sequence
   int t0, head;                          // first token (within the sequence), KV head
-  int n0, n1;                            // key tiles of each row tile
+  int first;                             // first key tile (of a split item)
+  int n0, n1;                            // key tiles of each row tile, from `first` on
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
 // Sequence and tile of work item `tile`, by one warp.  Lengths are clamped to
 // the packed tensors, so no array content leads out of them.
-__device__ bool find_item(const Args& a, int tile, int head, Item* it) {
+// CTA `rank` of `split` takes its share of the item's key tiles.
+__device__ bool find_item(const Args& a, int tile, int head, int rank, int split, Item* it) {
   const int lane = threadIdx.x & 31;
   const int per = 2 * a.tokens;
   int before = 0;
@@ -89,8 +112,11 @@ __device__ bool find_item(const Args& a, int tile, int head, Item* it) {
         const int mid = min(t0 + a.tokens, lq), end = min(t0 + per, lq);
         const int seen0 = a.causal ? clampi(lk - lq + mid, 0, lk) : lk;
         const int seen1 = a.causal ? clampi(lk - lq + end, 0, lk) : lk;
-        it->n0 = (seen0 + kKeys - 1) / kKeys;
-        it->n1 = end > mid ? (seen1 + kKeys - 1) / kKeys : 0;
+        const int n0 = (seen0 + kKeys - 1) / kKeys, n1 = end > mid ? (seen1 + kKeys - 1) / kKeys : 0;
+        const int n = max(n0, n1), from = n * rank / split, to = n * (rank + 1) / split;
+        it->first = from;
+        it->n0 = clampi(n0 - from, 0, to - from);
+        it->n1 = clampi(n1 - from, 0, to - from);
       }
       return true;
     }
@@ -110,18 +136,20 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
   return false;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                             const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args a) {
-  constexpr int kBytes = Tile<D>::kBytes, kStages = Tile<D>::kStages;
+  using T = Tile<D, SPLIT>;
+  constexpr int kBytes = T::kBytes, kStages = T::kStages;
   constexpr int kHalf = kRows * 128;                    // one 64-channel column block of a tile
   constexpr uint32_t kTmem = 512, kOut = 256;           // scores at 0 and 128, outputs from 256
+  constexpr int kReaders = 11;                          // warps that read an item besides the one that finds it
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * Tile<D>::kStages + 13];
-  __shared__ Item s_item;
+  __shared__ __align__(16) uint8_t s_taken[16];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 23];
+  __shared__ Item s_item[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_found;
   __shared__ volatile int s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,17 +160,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
   const uint32_t rest = bar0 + 16u * kStages;
   auto q_full = [&](int w) { return rest + 8u * w; };
-  auto s_full = [&](int w) { return rest + 16u + 8u * w; };
-  auto p_full = [&](int w, int half) { return rest + 32u + 16u * w + 8u * half; };
-  auto o_full = [&](int w) { return rest + 64u + 8u * w; };
-  const uint32_t v_last = rest + 80u;
-  auto drained = [&](int w) { return rest + 88u + 8u * w; };
+  auto q_empty = [&](int w) { return rest + 16u + 8u * w; };
+  auto s_full = [&](int w) { return rest + 32u + 8u * w; };
+  auto p_full = [&](int w, int half) { return rest + 48u + 16u * w + 8u * half; };
+  auto o_full = [&](int w) { return rest + 80u + 8u * w; };
+  auto drained = [&](int w) { return rest + 96u + 8u * w; };
+  auto v_last = [&](int i) { return rest + 112u + 8u * (i & 1); };
+  auto item_full = [&](int k) { return rest + 128u + 8u * (k & 1); };
+  auto item_empty = [&](int k) { return rest + 144u + 8u * (k & 1); };
+  const uint32_t taken = rest + 160u;
 
   if (warp == 8) tmem_alloc(smem_addr(&s_tmem), kTmem);
-  if (warp == 9) {
-    const bool found = find_item(a, blockIdx.x / a.Hkv, blockIdx.x % a.Hkv, &s_item);
-    if (lane == 0) s_found = found;
-  }
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int s = 0; s < kStages; ++s) {
@@ -151,39 +179,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int w = 0; w < 2; ++w) {
       bar_init(q_full(w), 1);
+      bar_init(q_empty(w), 1);
       bar_init(s_full(w), 1);
       bar_init(p_full(w, 0), kRows);
       bar_init(p_full(w, 1), kRows);
       bar_init(o_full(w), 1);
       bar_init(drained(w), 1);
+      bar_init(v_last(w), 1);
+      bar_init(item_full(w), 1);
+      bar_init(item_empty(w), kReaders);
     }
-    bar_init(v_last, 1);
+    bar_init(taken, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
     tma_prefetch_map(&map_v);
   }
   fence_before();
-  __syncthreads();
+  if (SPLIT)
+    cg::this_cluster().sync();                          // the other CTAs' shared memory is there
+  else
+    __syncthreads();
   fence_after();
   const uint32_t tmem = s_tmem;
-  const bool found = s_found != 0;
 
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_on(bar, parity, &s_abort, a.status); };
+  auto all = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(bar, parity)); };
+  // Item k of this CTA, by a whole warp; false at the end of the work.
+  auto get_item = [&](int k, Item& it) {
+    if (!all(item_full(k), (k >> 1) & 1)) return false;
+    it = s_item[k & 1];
+    __syncwarp();
+    if (lane == 0) bar_arrive(item_empty(k));
+    return it.found != 0;
+  };
+  float ref = -INFINITY, l = 0.f;                       // softmax threads: the latest item's row
+  bool in_item = false;
 
   if (warp >= 8) {
     regs_dec<80>();
-    const Item it = s_item;
-    const int n = found ? max(it.n0, it.n1) : 0;
-    const bool partial = n * kKeys > it.lk;             // the last key tile ends behind the sequence
-    if ((warp == 8 || warp == 11) && n > 0) {
+    if (warp == 8 || warp == 11) {
       // ---------------------------------------------------------- products
       // A warp per row tile: a warp that has issued products goes on to its
       // next wait only when they are done, so one warp for both tiles leaves
       // the tensor cores idle between them.  The whole warp runs the role,
       // one lane issues.
       constexpr uint32_t dqk = mma_desc(kRows, kKeys, BF16, false), dpv = mma_desc(kRows, D, BF16, true);
-      const int w = warp == 11, nw = w ? it.n1 : it.n0;
+      const int w = warp == 11;
       const uint32_t scores = tmem + w * kKeys, output = tmem + kOut + w * D, q = desc_lo(sq + w * kBytes, 16);
       auto issue_s = [&](int stage) {
         const uint32_t k = desc_lo(skv + stage * kBytes, 16);
@@ -193,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss(scores, q + off, k + off, desc_hi(1024), dqk, i > 0);
         }
         mma_commit(s_full(w));
+        mma_commit(empty(stage));
       };
       auto issue_o = [&](int stage, int half, bool accumulate) {
         const uint32_t v = desc_lo(skv + stage * kBytes + half * (kHalf / 2), kHalf);
@@ -201,7 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kKeys / 32; ++i)
           mma_ts(output, p + 8 * i, v + i * (2048 >> 4), desc_hi(1024), dpv, accumulate || half > 0 || i > 0);
       };
-      auto all = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(bar, parity)); };
       bool ok = true;
       int stage = -1;                                   // the latest tile of the ring and its parity
       uint32_t parity = 0;
@@ -212,122 +255,189 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = ok && all(full(stage), parity);
       };
-      if (nw > 0) {
-        next_full();
-        ok = ok && all(q_full(w), 0);
-        if (ok) {
-          fence_after();
-          if (elect()) {
-            issue_s(0);
-            mma_commit(empty(0));
-          }
-          __syncwarp();
-        }
-      }
-      for (int j = 0; j < nw && ok; ++j) {
-        next_full();                                    // V of this tile
-        const int v = stage;
-        if (j + 1 < nw) next_full();                    // K of the next one
-        const int k = stage;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && all(p_full(w, half), j & 1);
-          if (!ok) break;
-          fence_after();
-          if (elect()) {
-            issue_o(v, half, j > 0);
-            if (half) {
-              if (j + 1 < nw) {
-                issue_s(k);
-                mma_commit(empty(k));
-              } else {
-                mma_commit(o_full(w));
-              }
-              mma_commit(empty(v));
+      uint32_t tiles = 0, items = 0;                    // done by this warp: parities of its barriers
+      Item it;
+      for (int k = 0; ok && get_item(k, it); ++k) {
+        const int nw = w ? it.n1 : it.n0, n = max(it.n0, it.n1);
+        if (nw > 0) {
+          next_full();
+          ok = ok && all(q_full(w), items & 1);
+          if (ok) {
+            fence_after();
+            if (elect()) {
+              issue_s(stage);
+              if (nw == 1) mma_commit(q_empty(w));
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
+        for (int j = 0; j < nw && ok; ++j) {
+          next_full();                                  // V of this tile
+          const int v = stage;
+          if (j + 1 < nw) next_full();                  // K of the next one
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && all(p_full(w, half), (tiles + j) & 1);
+            if (!ok) break;
+            fence_after();
+            if (elect()) {
+              issue_o(v, half, j > 0);
+              if (half) {
+                if (j + 1 < nw) {
+                  issue_s(stage);
+                  if (j + 2 == nw) mma_commit(q_empty(w));
+                } else {
+                  mma_commit(o_full(w));
+                }
+                mma_commit(empty(v));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        for (int i = 2 * nw; i < 2 * n && ok; ++i) {    // tiles that only the other row tile sees
+          next_full();
+          if (ok && lane == 0) bar_arrive(empty(stage));
+        }
+        tiles += nw;
+        items += nw > 0;
       }
-      for (int i = 2 * nw; i < 2 * n && ok; ++i) {      // tiles that only the other row tile sees
-        next_full();
-        if (ok && lane == 0) bar_arrive(empty(stage));
-      }
-      if (!ok && elect()) {                             // nothing in flight when the CTA ends
+      if (s_abort && elect()) {                         // nothing in flight when the CTA ends
         mma_commit(drained(w));
         for (int i = 0; i < kPolls && !bar_try(drained(w), 0); ++i) {}
       }
-    } else if (warp == 9 && lane == 0 && n > 0) {
+    } else if (warp == 9) {
       // ---------------------------------------------------------- copies
       const int q_bytes = a.tokens * a.G * D * 2;
-      auto load_q = [&](int w) {
-        if ((w ? it.n1 : it.n0) == 0) return;
-        bar_expect(q_full(w), q_bytes);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load(sq + w * kBytes + c * kHalf, &map_q, c * 64, it.head * a.G, it.q0 + it.t0 + w * a.tokens,
-                   q_full(w));
-      };
-      int issued = 0;
+      int count = 0, lasts = 0;                         // K and V tiles copied, v_last barriers used
+      uint32_t held = 0;                                // bit i: the copy i before the latest is on v_last
+      uint32_t queries[2] = {0, 0};
       bool ok = true;
-      load_q(0);
-      for (int i = 0; i < 2 * n; ++i) {
-        const int s = i % kStages;
-        if (i >= kStages && !wait(empty(s), (i / kStages - 1) & 1)) { ok = false; break; }
-        const uint32_t bar = partial && i == 2 * n - 1 ? v_last : full(s);
-        bar_expect(bar, kBytes);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load(skv + s * kBytes + c * kHalf, i & 1 ? &map_v : &map_k, c * 64, it.head, it.k0 + (i >> 1) * kKeys,
-                   bar);
-        ++issued;
-        if (i == 0) load_q(1);
+      Item it;
+      for (int k = 0; ok && get_item(k, it); ++k) {
+        const int n = max(it.n0, it.n1);
+        const bool partial = (it.first + n) * kKeys > it.lk;     // the last tile ends behind the sequence
+        if (lane == 0) {
+          auto load_q = [&](int w) {
+            if ((w ? it.n1 : it.n0) == 0) return;
+            uint32_t& used = w ? queries[1] : queries[0];
+            if (used > 0) ok = ok && wait(q_empty(w), (used - 1) & 1);
+            if (!ok) return;
+            ++used;
+            bar_expect(q_full(w), q_bytes);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load(sq + w * kBytes + c * kHalf, &map_q, c * 64, it.head * a.G, it.q0 + it.t0 + w * a.tokens,
+                       q_full(w));
+          };
+          load_q(0);
+          for (int i = 0; i < 2 * n && ok; ++i) {
+            const int s = count % kStages;
+            if (count >= kStages) ok = wait(empty(s), (count / kStages - 1) & 1);
+            if (!ok) break;
+            const bool last = partial && i == 2 * n - 1;
+            const uint32_t bar = last ? v_last(lasts++) : full(s);
+            bar_expect(bar, kBytes);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load(skv + s * kBytes + c * kHalf, i & 1 ? &map_v : &map_k, c * 64, it.head,
+                       it.k0 + (it.first + (i >> 1)) * kKeys, bar);
+            held = held << 1 | last;
+            ++count;
+            if (i == 0) load_q(1);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (!ok) {
+      if (s_abort && lane == 0) {
+        auto drain = [&](uint32_t bar, uint32_t parity) {
+          for (int i = 0; i < kPolls && !bar_try(bar, parity); ++i) {}
+        };
         for (int w = 0; w < 2; ++w)
-          if (w ? it.n1 : it.n0)
-            for (int i = 0; i < kPolls && !bar_try(q_full(w), 0); ++i) {}
-        for (int j = max(0, issued - kStages); j < issued; ++j) {
-          const bool last = partial && j == 2 * n - 1;
-          for (int i = 0; i < kPolls && !bar_try(last ? v_last : full(j % kStages),
-                                                       last ? 0 : (j / kStages) & 1); ++i) {}
+          if (queries[w]) drain(q_full(w), (queries[w] - 1) & 1);
+        for (int i = 0; i < min(count, kStages); ++i)
+          if (!(held >> i & 1)) drain(full((count - 1 - i) % kStages), ((count - 1 - i) / kStages) & 1);
+        for (int i = max(0, lasts - 2); i < lasts; ++i) drain(v_last(i), (i >> 1) & 1);
+      }
+    } else {
+      // ------------------------------------------ items and the last V tile
+      const int split = SPLIT ? a.split : 1;
+      const int rank = SPLIT ? blockIdx.x % split : 0;
+      int index = blockIdx.x / split;                   // of the item (a CTA or a cluster each)
+      Item it;
+      auto publish = [&](int k) {
+        if (k >= 2 && !all(item_empty(k), ((k >> 1) - 1) & 1)) return false;
+        const bool found =
+            index >= 0 && find_item(a, index / a.Hkv, index % a.Hkv, rank, split, &s_item[k & 1]);
+        __syncwarp();
+        if (lane == 0) {
+          s_item[k & 1].found = found;
+          bar_arrive(item_full(k));
+        }
+        __syncwarp();
+        it = s_item[k & 1];
+        return found;
+      };
+      int lasts = 0, stage = 0;                         // partial tiles cleared, ring position of the item
+      bool more = publish(0);
+      for (int k = 0; more; ++k) {
+        const Item now = it;
+        const int n = max(now.n0, now.n1);
+        index = -1;
+        if (!SPLIT) {
+          if (lane == 0) {
+            take_cta(smem_addr(s_taken), taken);
+            for (int i = 0; i < kPolls && !bar_try(taken, k & 1); ++i) {}
+          }
+          __syncwarp();
+          index = all(taken, k & 1) ? taken_cta(smem_addr(s_taken)) : -1;
+          __syncwarp();
+        }
+        more = publish(k + 1);
+        stage = (stage + 2 * n) % kStages;              // behind this item's last tile
+        if (n > 0 && (now.first + n) * kKeys > now.lk) {
+          // The last key tile also holds rows behind the sequence: of the
+          // next one, whatever they are.  Their weights are zero, but zero
+          // times an infinity or NaN is not: those rows of V are cleared
+          // before the tile is passed on.
+          const int s = (stage + kStages - 1) % kStages;
+          const uint32_t bar = v_last(lasts);
+          if (!all(bar, (lasts >> 1) & 1)) break;
+          ++lasts;
+          const int first = now.lk - (now.first + n - 1) * kKeys;
+          for (int c = 0; c < D / 64; ++c)
+            for (int i = first * 8 + lane; i < kKeys * 8; i += 32)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(skv + s * kBytes + c * kHalf + i * 16),
+                           "r"(0)
+                           : "memory");
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          __syncwarp();
+          if (lane == 0) bar_arrive(full(s));
         }
       }
-    } else if (warp == 10 && n > 0 && partial) {
-      // The last key tile also holds rows behind the sequence: of the next
-      // one, whatever they are.  Their probabilities are zero, but zero times
-      // an infinity or NaN is not: those rows of V are cleared before the
-      // tile is passed on.
-      const int s = (2 * n - 1) % kStages;
-      if (__all_sync(0xffffffffu, wait(v_last, 0))) {
-        const int first = it.lk - (n - 1) * kKeys;
-        for (int c = 0; c < D / 64; ++c)
-          for (int i = first * 8 + lane; i < kKeys * 8; i += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(skv + s * kBytes + c * kHalf + i * 16),
-                         "r"(0)
-                         : "memory");
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(full(s));
-      }
     }
+    __syncwarp();
+    regs_inc<kRegs>();                                  // all warps go on with the launch's count
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<208>();
-    const Item it = s_item;
     const int w = warp >> 2, row = threadIdx.x & 127;
-    const int nw = w ? it.n1 : it.n0;                   // key tiles of this row tile
-    if (found && it.t0 + w * a.tokens < it.lq) {
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
+    const uint32_t ts = tmem + w * kKeys + lane_base, to = tmem + kOut + w * D + lane_base;
+    uint32_t tiles = 0, items = 0;                      // done by this warpgroup: parities of its barriers
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok && get_item(k, it); ++k) {
+      const int nw = w ? it.n1 : it.n0;                 // key tiles of this row tile
+      if (it.t0 + w * a.tokens >= it.lq) continue;
       const int t = it.t0 + w * a.tokens + row / a.G;
       const bool valid = row < a.tokens * a.G && t < it.lq;
       const int seen = !valid ? 0 : a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
-      const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
-      const uint32_t ts = tmem + w * kKeys + lane_base, to = tmem + kOut + w * D + lane_base;
-      float ref = -INFINITY, l = 0.f;                   // reference of the exponentials, their sum
-      bool ok = true;
+      ref = -INFINITY;                                  // reference of the exponentials, and their sum
+      l = 0.f;
       for (int j = 0; j < nw; ++j) {
-        ok = __all_sync(0xffffffffu, wait(s_full(w), j & 1));
+        ok = all(s_full(w), (tiles + j) & 1);
         if (!ok) break;
         fence_after();
-        const int left = seen - j * kKeys;              // keys of the tile that the row sees
+        const int left = seen - (it.first + j) * kKeys; // keys of the tile that the row sees
         const bool masked = __any_sync(0xffffffffu, left < kKeys);
         uint32_t s[kKeys];
         float m[4] = {ref, ref, ref, ref};
@@ -390,54 +500,121 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 both = (sum[0] + sum[1]).get();
         l += both.x + both.y;
       }
-      if (ok && nw > 0) {
-        ok = __all_sync(0xffffffffu, wait(o_full(w), 0));
+      tiles += nw;
+      if (!ok) break;
+      if (nw > 0) {
+        ok = all(o_full(w), items & 1);
+        if (!ok) break;
         fence_after();
+        ++items;
       }
-      if (ok) {
-        // Rows without a key are zero.  The row goes through the warp's own
-        // part of the Q tile, so that the stores are whole rows.
-        const float inv = seen > 0 ? 1.f / l : 0.f;
-        uint8_t* stage = smem + w * kBytes;
+      if (SPLIT) {
+        in_item = true;
+        continue;                                       // merged below
+      }
+      // Rows without a key are zero.
+      const float inv = seen > 0 ? 1.f / l : 0.f;
+      uint16_t* dst = a.out + (long long)(it.q0 + t) * a.out_token + (long long)(it.head * a.G + row % a.G) * a.out_head;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          if (nw > 0) {
-            tmem_ld32(to + c, o);
-            wait_ld32(o);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (seen > 0) {
-              x.x = pack2<BF16>(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
-              x.y = pack2<BF16>(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
-              x.z = pack2<BF16>(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
-              x.w = pack2<BF16>(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
-            }
-            const int chunk = (c & 63) / 8 + i;
-            *reinterpret_cast<uint4*>(stage + (c >> 6) * kHalf + row * 128 + ((chunk ^ (row & 7)) << 4)) = x;
-          }
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (nw > 0) {
+          tmem_ld32(to + c, o);
+          wait_ld32(o);
         }
-        if (a.lse && valid) {
-          const float lse = seen > 0 ? (ref == -INFINITY ? 0.f : ref * a.scale) + logf(l) : -INFINITY;
-          a.lse[(long long)(it.q0 + t) * a.Hq + it.head * a.G + row % a.G] = lse;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          o[i] = seen > 0 ? pack2<BF16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0;
+        if (valid) {
+          if (a.wide) {
+            st_global32(dst + c, o);
+            st_global32(dst + c + 16, o + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(dst + c + 2 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
         }
         __syncwarp();
-        constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
-        const int chunk = lane % kChunks;
-        for (int i = 0; i < 32; i += kRowsAtOnce) {
-          const int r = (warp & 3) * 32 + i + lane / kChunks;
-          const int tr = it.t0 + w * a.tokens + r / a.G;
-          if (r < a.tokens * a.G && tr < it.lq) {
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * kHalf + r * 128 +
-                                                            (((chunk & 7) ^ (r & 7)) << 4));
-            *reinterpret_cast<uint4*>(a.out + (long long)(it.q0 + tr) * a.out_token +
-                                      (long long)(it.head * a.G + r % a.G) * a.out_head + chunk * 8) = x;
-          }
+      }
+      fence_before();                                   // the next product overwrites the accumulator
+      if (a.lse && valid)
+        a.lse[(long long)(it.q0 + t) * a.Hq + it.head * a.G + row % a.G] =
+            seen > 0 ? (ref == -INFINITY ? 0.f : ref * a.scale) + logf(l) : -INFINITY;
+    }
+    __syncwarp();
+    regs_dec<kRegs>();
+  }
+
+  if (SPLIT) {
+    // ---------------------------------------------------------------- merge
+    // Every CTA sends (reference, sum) of its rows to all of the cluster,
+    // scales its part of the output to the common reference and sum, and adds
+    // up the parts of its share of the rows.
+    cg::cluster_group cluster = cg::this_cluster();
+    const int split = a.split, rank = blockIdx.x % split;
+    float* part = reinterpret_cast<float*>(smem);       // [2 * kRows][kPitch], over the tiles
+    float2* sums = reinterpret_cast<float2*>(smem + (2 + kStages) * kBytes);   // [split][2 * kRows]
+    if (threadIdx.x < 2 * kRows)
+      for (int r = 0; r < split; ++r)
+        *cluster.map_shared_rank(&sums[rank * 2 * kRows + threadIdx.x], r) = make_float2(ref, l);
+    cluster.sync();
+    const Item it = s_item[0];
+    const bool done = it.found != 0 && !s_abort;
+    if (threadIdx.x < 2 * kRows && in_item && done) {
+      const int w = warp >> 2, row = threadIdx.x & 127, nw = w ? it.n1 : it.n0;
+      const int t = it.t0 + w * a.tokens + row / a.G;
+      const bool valid = row < a.tokens * a.G && t < it.lq;
+      const int seen = !valid ? 0 : a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
+      float top = -INFINITY, sum = 0.f;
+      for (int r = 0; r < split; ++r) top = fmaxf(top, sums[r * 2 * kRows + threadIdx.x].x);
+      for (int r = 0; r < split; ++r) {
+        const float2 x = sums[r * 2 * kRows + threadIdx.x];
+        sum += x.y * (x.x == top ? 1.f : ex2((x.x - top) * a.scale2));
+      }
+      const float f = seen > 0 ? (ref == top ? 1.f : ex2((ref - top) * a.scale2)) / sum : 0.f;
+      const uint32_t to = tmem + kOut + w * D + ((uint32_t)(warp & 3) << 21);
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (nw > 0) {
+          tmem_ld32(to + c, o);
+          wait_ld32(o);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (nw > 0 && seen > 0)
+            x = make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f, __uint_as_float(o[i + 2]) * f,
+                            __uint_as_float(o[i + 3]) * f);
+          *reinterpret_cast<float4*>(part + threadIdx.x * T::kPitch + c + i) = x;
         }
       }
+      if (a.lse && valid && rank == 0)
+        a.lse[(long long)(it.q0 + t) * a.Hq + it.head * a.G + row % a.G] =
+            seen > 0 ? (top == -INFINITY ? 0.f : top * a.scale) + logf(sum) : -INFINITY;
     }
+    cluster.sync();
+    if (done) {
+      const int per = a.tokens * a.G;                   // rows of a tile that are used
+      const int rows = min(2 * a.tokens, it.lq - it.t0) * a.G;
+      constexpr int kVec = D / 32;                      // channels per lane
+      for (int i = rank + split * warp; i < rows; i += split * (kThreads / 32)) {
+        const int slot = i < per ? i : kRows + i - per;
+        float x[kVec] = {};
+        for (int r = 0; r < split; ++r) {
+          const float* src = cluster.map_shared_rank(part, r) + slot * T::kPitch + lane * kVec;
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) x[j] += src[j];
+        }
+        const int t = it.t0 + i / a.G;
+        uint16_t* dst = a.out + (long long)(it.q0 + t) * a.out_token +
+                        (long long)(it.head * a.G + i % a.G) * a.out_head + lane * kVec;
+#pragma unroll
+        for (int j = 0; j < kVec; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<BF16>(x[j], x[j + 1]);
+      }
+    }
+    cluster.sync();                                     // no CTA leaves while another reads its part
   }
   fence_before();
   __syncthreads();
@@ -496,17 +673,54 @@ int status_word(int32_t** out) {
   return CONFKV_OK;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, long long items,
            cudaStream_t st) {
   static int done[kMaxDevices] = {};
-  auto kernel = prompt_attention_kernel<D, BF16>;
+  auto kernel = prompt_attention_kernel<D, BF16, SPLIT>;
+  constexpr int smem = Tile<D, SPLIT>::kSmem;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    if (ensure_smem(kernel, Tile<D>::kSmem, done) != cudaSuccess) return CONFKV_ECUDA;
+    if (ensure_smem(kernel, smem, done) != cudaSuccess) return CONFKV_ECUDA;
   }
-  kernel<<<(unsigned)items, kThreads, Tile<D>::kSmem, st>>>(mq, mk, mv, a);
-  return cudaGetLastError() == cudaSuccess ? CONFKV_OK : CONFKV_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * a.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a) == cudaSuccess ? CONFKV_OK : CONFKV_ECUDA;
+}
+
+template <int D, bool BF16>
+int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, long long items,
+           cudaStream_t st) {
+  return a.split > 1 ? launch<D, BF16, true>(mq, mk, mv, a, items, st)
+                     : launch<D, BF16, false>(mq, mk, mv, a, items, st);
+}
+
+// CTAs that share an item's keys, from what the host knows: the largest
+// number of items and the average number of key tiles of a sequence.  Time is
+// taken as rounds of the SMs times (tiles of a CTA + the tiles that its start
+// and its merge cost).
+int choose_split(long long items, double tiles) {
+  if (items >= 4LL * 152) return 1;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= kMaxSplit; s *= 2) {
+    const double rounds = std::max(1.0, (double)items * s / 152.0);
+    const double t = (s == 1 ? std::ceil(rounds) : rounds) * (std::ceil(tiles / s) + (s == 1 ? 3.0 : 4.0));
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
 }
 
 bool rows_ok(const void* p, const int64_t* stride, int d, long long tokens, long long heads) {
@@ -551,7 +765,10 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
   a.scale2 = p->scale * 1.4426950408889634f;
   // no more tiles than these, whatever the lengths
   const long long tiles = (long long)p->total_q / (2 * a.tokens) + p->B;
-  if (tiles * p->Hkv >= (1LL << 31)) return CONFKV_EINVAL;
+  if (tiles * p->Hkv >= (1LL << 31) / kMaxSplit) return CONFKV_EINVAL;
+  a.split = choose_split(tiles * p->Hkv, (double)p->total_k / p->B / kKeys);
+  a.wide = reinterpret_cast<uintptr_t>(p->out) % 32 == 0 && (p->total_q < 2 || p->out_stride[0] % 16 == 0) &&
+           (p->Hq < 2 || p->out_stride[1] % 16 == 0);
   const bool bf16 = p->dtype == CONFKV_Q_BF16;
   if (!encode_fn()) return CONFKV_ECUDA;
   CUtensorMap mq, mk, mv;

@@ -47,6 +47,31 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
 
+// ------------------------------------------------------------- work of other CTAs
+// Takes over the work of a CTA of this grid that has not started: its index
+// arrives in the 16 bytes at `response`, completing `bar`.  Not to be asked
+// again after a refusal.
+__device__ __forceinline__ void take_cta(uint32_t response, uint32_t bar) {
+  bar_expect(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(
+                   response),
+               "r"(bar)
+               : "memory");
+}
+// The index taken over, or -1 if there was none.
+__device__ __forceinline__ int taken_cta(uint32_t response) {
+  int x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z, w;\n ld.shared.b128 r, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n mov.b32 %0, -1;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n"
+      " fence.proxy.async.shared::cta;\n}\n"
+      : "=r"(x)
+      : "r"(response)
+      : "memory");
+  return x;
+}
+
 // ------------------------------------------------------------- tensor memory
 __device__ __forceinline__ void tmem_alloc(uint32_t result, uint32_t columns) {   // one whole warp
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(result), "r"(columns)
@@ -168,6 +193,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+// 32 bytes in one store (32-byte aligned).
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // Two fp32 values as fp16 or bf16 pairs, `lo` in the low half.
 template <bool BF16>
