@@ -22,6 +22,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/confkv.h"
 #include "confkv_internal.cuh"
@@ -48,7 +49,7 @@ struct Tile {
   static constexpr int kBytes = kRows * D * 2;         // a Q, K or V tile
   // K and V tiles in flight; a split item needs room for the merge
   static constexpr int kStages = (D == 128 ? 5 : 8) - (SPLIT ? 1 : 0);
-  static constexpr int kMerge = SPLIT ? kMaxSplit * 2 * kRows * 8 : 0;
+  static constexpr int kMerge = SPLIT ? 2 * kRows * 8 : 0;
   static constexpr int kSmem = (2 + kStages) * kBytes + kMerge + 1024;
   static constexpr int kPitch = D + 4;                 // floats per row of a part
   static_assert(!SPLIT || 2 * kRows * kPitch * 4 <= (2 + kStages) * kBytes, "a part fits the tiles' place");
@@ -57,6 +58,7 @@ struct Tile {
 struct Args {
   int B, Hq, Hkv, G, tokens;             // tokens: per 128-row tile
   int split;                             // CTAs per item
+  int item0;                             // first item of the launch
   int causal;
   int total_q, total_k;
   const int32_t* cu_q;
@@ -88,10 +90,13 @@ __device__ bool find_item(const Args& a, int tile, int head, int rank, int split
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    int q0 = 0, lq = 0;
+    int q0 = 0, lq = 0, k0 = 0, lk = 0;
     if (b < a.B) {
-      q0 = clampi(a.cu_q[b], 0, a.total_q);
-      lq = clampi(a.cu_q[b + 1], q0, a.total_q) - q0;
+      const int qa = a.cu_q[b], qb = a.cu_q[b + 1], ka = a.cu_k[b], kb = a.cu_k[b + 1];
+      q0 = clampi(qa, 0, a.total_q);
+      lq = clampi(qb, q0, a.total_q) - q0;
+      k0 = clampi(ka, 0, a.total_k);
+      lk = clampi(kb, k0, a.total_k) - k0;
     }
     const int nt = (lq + per - 1) / per;
     int sum = nt;
@@ -104,8 +109,6 @@ __device__ bool find_item(const Args& a, int tile, int head, int rank, int split
     const unsigned hit = __ballot_sync(0xffffffffu, mine);
     if (hit) {
       if (mine) {
-        const int k0 = clampi(a.cu_k[b], 0, a.total_k);
-        const int lk = clampi(a.cu_k[b + 1], k0, a.total_k) - k0;
         const int t0 = (nt - 1 - (tile - (before + sum - nt))) * per;   // the longest rows first
         it->q0 = q0; it->lq = lq; it->k0 = k0; it->lk = lk;
         it->t0 = t0; it->head = head;
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kReaders = 11;                          // warps that read an item besides the one that finds it
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) uint8_t s_taken[16];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 23];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 20];
   __shared__ Item s_item[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
@@ -162,13 +165,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto q_full = [&](int w) { return rest + 8u * w; };
   auto q_empty = [&](int w) { return rest + 16u + 8u * w; };
   auto s_full = [&](int w) { return rest + 32u + 8u * w; };
-  auto p_full = [&](int w, int half) { return rest + 48u + 16u * w + 8u * half; };
-  auto o_full = [&](int w) { return rest + 80u + 8u * w; };
-  auto drained = [&](int w) { return rest + 96u + 8u * w; };
-  auto v_last = [&](int i) { return rest + 112u + 8u * (i & 1); };
-  auto item_full = [&](int k) { return rest + 128u + 8u * (k & 1); };
-  auto item_empty = [&](int k) { return rest + 144u + 8u * (k & 1); };
-  const uint32_t taken = rest + 160u;
+  auto p_full = [&](int w) { return rest + 48u + 8u * w; };
+  auto o_full = [&](int w) { return rest + 64u + 8u * w; };
+  auto drained = [&](int w) { return rest + 80u + 8u * w; };
+  auto v_last = [&](int i) { return rest + 96u + 8u * (i & 1); };
+  auto item_full = [&](int k) { return rest + 112u + 8u * (k & 1); };
+  auto item_empty = [&](int k) { return rest + 128u + 8u * (k & 1); };
+  const uint32_t taken = rest + 144u, copied = rest + 152u;
 
   if (warp == 8) tmem_alloc(smem_addr(&s_tmem), kTmem);
   if (threadIdx.x == 0) {
@@ -181,8 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(q_full(w), 1);
       bar_init(q_empty(w), 1);
       bar_init(s_full(w), 1);
-      bar_init(p_full(w, 0), kRows);
-      bar_init(p_full(w, 1), kRows);
+      bar_init(p_full(w), kRows);
       bar_init(o_full(w), 1);
       bar_init(drained(w), 1);
       bar_init(v_last(w), 1);
@@ -190,11 +192,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(item_empty(w), kReaders);
     }
     bar_init(taken, 1);
+    bar_init(copied, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
     tma_prefetch_map(&map_v);
+  }
+  // what the CTA starts with, while the barriers are set up
+  const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0;
+  if (warp == 10) {
+    const int index = a.item0 + blockIdx.x / split;     // an item per CTA, or per cluster
+    const bool found = find_item(a, index / a.Hkv, index % a.Hkv, rank, split, &s_item[0]);
+    if (lane == 0) s_item[0].found = found;
   }
   fence_before();
   if (SPLIT)
@@ -208,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto all = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(bar, parity)); };
   // Item k of this CTA, by a whole warp; false at the end of the work.
   auto get_item = [&](int k, Item& it) {
-    if (!all(item_full(k), (k >> 1) & 1)) return false;
+    if (k > 0 && !all(item_full(k), (k - 1) >> 1 & 1)) return false;   // item 0 is there from the start
     it = s_item[k & 1];
     __syncwarp();
     if (lane == 0) bar_arrive(item_empty(k));
@@ -238,12 +248,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(s_full(w));
         mma_commit(empty(stage));
       };
-      auto issue_o = [&](int stage, int half, bool accumulate) {
-        const uint32_t v = desc_lo(skv + stage * kBytes + half * (kHalf / 2), kHalf);
-        const uint32_t p = scores + half * (kKeys / 4);
+      auto issue_o = [&](int stage, bool accumulate) {
+        const uint32_t v = desc_lo(skv + stage * kBytes, kHalf);
 #pragma unroll
-        for (int i = 0; i < kKeys / 32; ++i)
-          mma_ts(output, p + 8 * i, v + i * (2048 >> 4), desc_hi(1024), dpv, accumulate || half > 0 || i > 0);
+        for (int i = 0; i < kKeys / 16; ++i)
+          mma_ts(output, scores + 8 * i, v + i * (2048 >> 4), desc_hi(1024), dpv, accumulate || i > 0);
       };
       bool ok = true;
       int stage = -1;                                   // the latest tile of the ring and its parity
@@ -275,25 +284,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_full();                                  // V of this tile
           const int v = stage;
           if (j + 1 < nw) next_full();                  // K of the next one
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && all(p_full(w, half), (tiles + j) & 1);
-            if (!ok) break;
-            fence_after();
-            if (elect()) {
-              issue_o(v, half, j > 0);
-              if (half) {
-                if (j + 1 < nw) {
-                  issue_s(stage);
-                  if (j + 2 == nw) mma_commit(q_empty(w));
-                } else {
-                  mma_commit(o_full(w));
-                }
-                mma_commit(empty(v));
-              }
+          ok = ok && all(p_full(w), (tiles + j) & 1);
+          if (!ok) break;
+          fence_after();
+          if (elect()) {
+            issue_o(v, j > 0);
+            if (j + 1 < nw) {
+              issue_s(stage);
+              if (j + 2 == nw) mma_commit(q_empty(w));
+            } else {
+              mma_commit(o_full(w));
             }
-            __syncwarp();
+            mma_commit(empty(v));
           }
+          __syncwarp();
         }
         for (int i = 2 * nw; i < 2 * n && ok; ++i) {    // tiles that only the other row tile sees
           next_full();
@@ -344,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++count;
             if (i == 0) load_q(1);
           }
+          bar_arrive(copied);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
@@ -359,14 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ------------------------------------------ items and the last V tile
-      const int split = SPLIT ? a.split : 1;
-      const int rank = SPLIT ? blockIdx.x % split : 0;
-      int index = blockIdx.x / split;                   // of the item (a CTA or a cluster each)
-      Item it;
-      auto publish = [&](int k) {
+      Item it = s_item[0];
+      auto publish = [&](int k, int index) {            // index: the CTA taken over, -1 for none
         if (k >= 2 && !all(item_empty(k), ((k >> 1) - 1) & 1)) return false;
+        index += a.item0;
         const bool found =
-            index >= 0 && find_item(a, index / a.Hkv, index % a.Hkv, rank, split, &s_item[k & 1]);
+            index >= a.item0 && find_item(a, index / a.Hkv, index % a.Hkv, rank, split, &s_item[k & 1]);
         __syncwarp();
         if (lane == 0) {
           s_item[k & 1].found = found;
@@ -377,12 +380,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         return found;
       };
       int lasts = 0, stage = 0;                         // partial tiles cleared, ring position of the item
-      bool more = publish(0);
+      bool more = it.found != 0;
       for (int k = 0; more; ++k) {
         const Item now = it;
         const int n = max(now.n0, now.n1);
-        index = -1;
+        int index = -1;
         if (!SPLIT) {
+          // Once the last copies of this item are issued: early enough for
+          // the next ones to follow them, and no item is held by a CTA that
+          // is long busy with another one.
+          if (!all(copied, k & 1)) break;
           if (lane == 0) {
             take_cta(smem_addr(s_taken), taken);
             for (int i = 0; i < kPolls && !bar_try(taken, k & 1); ++i) {}
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           index = all(taken, k & 1) ? taken_cta(smem_addr(s_taken)) : -1;
           __syncwarp();
         }
-        more = publish(k + 1);
+        more = publish(k + 1, index);
         stage = (stage + 2 * n) % kStages;              // behind this item's last tile
         if (n > 0 && (now.first + n) * kKeys > now.lk) {
           // The last key tile also holds rows behind the sequence: of the
@@ -414,8 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // All warps go on with the launch's register count.  The softmax warps
+    // give theirs back first: without the barrier, warps that have nothing to
+    // do could take registers that a softmax warpgroup has yet to ask for,
+    // and both would wait for ever.
     __syncwarp();
-    regs_inc<kRegs>();                                  // all warps go on with the launch's count
+    bar_sync<1>(kThreads);
+    regs_inc<kRegs>();
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<208>();
@@ -491,12 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[i] = pack2<BF16>(x, y);
           }
           tmem_st16(ts + c / 2, p);
-          if (c & 32) {                                 // the product starts with the first half
-            wait_st();
-            fence_before();
-            bar_arrive(p_full(w, c / 64));
-          }
         }
+        wait_st();
+        fence_before();
+        bar_arrive(p_full(w));
         const float2 both = (sum[0] + sum[1]).get();
         l += both.x + both.y;
       }
@@ -544,74 +554,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     regs_dec<kRegs>();
+    bar_sync<1>(kThreads);
   }
 
   if (SPLIT) {
     // ---------------------------------------------------------------- merge
-    // Every CTA sends (reference, sum) of its rows to all of the cluster,
-    // scales its part of the output to the common reference and sum, and adds
-    // up the parts of its share of the rows.
+    // Every CTA leaves (reference, sum) and output of its rows in its shared
+    // memory; each adds up the parts of its share of the rows.
     cg::cluster_group cluster = cg::this_cluster();
-    const int split = a.split, rank = blockIdx.x % split;
     float* part = reinterpret_cast<float*>(smem);       // [2 * kRows][kPitch], over the tiles
-    float2* sums = reinterpret_cast<float2*>(smem + (2 + kStages) * kBytes);   // [split][2 * kRows]
-    if (threadIdx.x < 2 * kRows)
-      for (int r = 0; r < split; ++r)
-        *cluster.map_shared_rank(&sums[rank * 2 * kRows + threadIdx.x], r) = make_float2(ref, l);
-    cluster.sync();
+    float2* sums = reinterpret_cast<float2*>(smem + (2 + kStages) * kBytes);   // [2 * kRows]
     const Item it = s_item[0];
+    __syncthreads();                                    // the products of both row tiles are done
     const bool done = it.found != 0 && !s_abort;
     if (threadIdx.x < 2 * kRows && in_item && done) {
-      const int w = warp >> 2, row = threadIdx.x & 127, nw = w ? it.n1 : it.n0;
-      const int t = it.t0 + w * a.tokens + row / a.G;
-      const bool valid = row < a.tokens * a.G && t < it.lq;
-      const int seen = !valid ? 0 : a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
-      float top = -INFINITY, sum = 0.f;
-      for (int r = 0; r < split; ++r) top = fmaxf(top, sums[r * 2 * kRows + threadIdx.x].x);
-      for (int r = 0; r < split; ++r) {
-        const float2 x = sums[r * 2 * kRows + threadIdx.x];
-        sum += x.y * (x.x == top ? 1.f : ex2((x.x - top) * a.scale2));
-      }
-      const float f = seen > 0 ? (ref == top ? 1.f : ex2((ref - top) * a.scale2)) / sum : 0.f;
+      const int w = warp >> 2, nw = w ? it.n1 : it.n0;
+      sums[threadIdx.x] = make_float2(ref, l);
       const uint32_t to = tmem + kOut + w * D + ((uint32_t)(warp & 3) << 21);
+      const int rows = min(a.tokens, it.lq - it.t0 - w * a.tokens) * a.G;
+      if ((warp & 3) * 32 < rows) {                     // warps with a row that is used
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (nw > 0) {
-          tmem_ld32(to + c, o);
-          wait_ld32(o);
-        }
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (nw > 0) {
+            tmem_ld32(to + c, o);
+            wait_ld32(o);
+          }
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (nw > 0 && seen > 0)
-            x = make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f, __uint_as_float(o[i + 2]) * f,
-                            __uint_as_float(o[i + 3]) * f);
-          *reinterpret_cast<float4*>(part + threadIdx.x * T::kPitch + c + i) = x;
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(part + threadIdx.x * T::kPitch + c + i) =
+                nw > 0 ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
         }
       }
-      if (a.lse && valid && rank == 0)
-        a.lse[(long long)(it.q0 + t) * a.Hq + it.head * a.G + row % a.G] =
-            seen > 0 ? (top == -INFINITY ? 0.f : top * a.scale) + logf(sum) : -INFINITY;
     }
     cluster.sync();
     if (done) {
       const int per = a.tokens * a.G;                   // rows of a tile that are used
       const int rows = min(2 * a.tokens, it.lq - it.t0) * a.G;
       constexpr int kVec = D / 32;                      // channels per lane
+      using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
       for (int i = rank + split * warp; i < rows; i += split * (kThreads / 32)) {
-        const int slot = i < per ? i : kRows + i - per;
-        float x[kVec] = {};
-        for (int r = 0; r < split; ++r) {
-          const float* src = cluster.map_shared_rank(part, r) + slot * T::kPitch + lane * kVec;
+        const int slot = i < per ? i : kRows + i - per, t = it.t0 + i / a.G;
+        const int seen = a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
+        Vec y[kMaxSplit];
+        float2 z[kMaxSplit];
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) x[j] += src[j];
-        }
-        const int t = it.t0 + i / a.G;
+        for (int r = 0; r < kMaxSplit; ++r)             // all parts in flight
+          if (r < split) {
+            y[r] = *reinterpret_cast<const Vec*>(cluster.map_shared_rank(part, r) + slot * T::kPitch + lane * kVec);
+            z[r] = *(cluster.map_shared_rank(sums, r) + slot);
+          }
+        float top = -INFINITY, sum = 0.f, x[kVec] = {};
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+          if (r < split) top = fmaxf(top, z[r].x);
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+          if (r < split) {
+            const float f = z[r].x == top ? 1.f : ex2((z[r].x - top) * a.scale2);
+            sum += z[r].y * f;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) x[j] += reinterpret_cast<const float*>(&y[r])[j] * f;
+          }
+        const float inv = 1.f / sum;
         uint16_t* dst = a.out + (long long)(it.q0 + t) * a.out_token +
                         (long long)(it.head * a.G + i % a.G) * a.out_head + lane * kVec;
 #pragma unroll
-        for (int j = 0; j < kVec; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<BF16>(x[j], x[j + 1]);
+        for (int j = 0; j < kVec; j += 2)
+          *reinterpret_cast<uint32_t*>(dst + j) = seen > 0 ? pack2<BF16>(x[j] * inv, x[j + 1] * inv) : 0;
+        if (a.lse && lane == 0)
+          a.lse[(long long)(it.q0 + t) * a.Hq + it.head * a.G + i % a.G] =
+              seen > 0 ? (top == -INFINITY ? 0.f : top * a.scale) + logf(sum) : -INFINITY;
       }
     }
     cluster.sync();                                     // no CTA leaves while another reads its part

@@ -33,6 +33,12 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Barrier ID over `threads` threads of converged warps.
+template <int ID>
+__device__ __forceinline__ void bar_sync(int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"n"(ID), "r"(threads) : "memory");
+}
+
 // ------------------------------------------------------------- TMA
 // Box at (x, head, token) of a (channel, head, token) tensor map.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int head, int token,
