@@ -39,7 +39,6 @@ using namespace tc;
 constexpr int kRows = 128;               // score rows per tile
 constexpr int kKeys = 128;               // keys per tile
 constexpr int kThreads = 384;            // two softmax warpgroups, one for copies and products
-constexpr int kPolls = 1 << 24;          // polls per wait (a few seconds at most)
 
 constexpr int kRegs = 168;               // registers a thread at launch: 65536 / 384, in eights
 constexpr int kMaxSplit = 8;             // CTAs of a cluster that share an item
@@ -128,12 +127,15 @@ __device__ bool find_item(const Args& a, int tile, int head, int rank, int split
   return false;
 }
 
-// Bounded wait; false once it, or another wait of the CTA, has given up.
+// Bounded wait (about four seconds); false once it, or another wait of the
+// CTA, has given up.
 __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  for (int i = 0; i < kPolls; ++i) {
+  if (bar_try(bar, parity)) return true;
+  const long long start = clock64();
+  do {
     if (bar_try(bar, parity)) return true;
     if (*abort) return false;
-  }
+  } while (clock64() - start < (1LL << 33));
   *abort = 1;
   atomicOr(status, kStatusTimeout);
   return false;
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (s_abort && elect()) {                         // nothing in flight when the CTA ends
         mma_commit(drained(w));
-        for (int i = 0; i < kPolls && !bar_try(drained(w), 0); ++i) {}
+        bar_wait(drained(w), 0);
       }
     } else if (warp == 9) {
       // ---------------------------------------------------------- copies
@@ -353,14 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       if (s_abort && lane == 0) {
-        auto drain = [&](uint32_t bar, uint32_t parity) {
-          for (int i = 0; i < kPolls && !bar_try(bar, parity); ++i) {}
-        };
         for (int w = 0; w < 2; ++w)
-          if (queries[w]) drain(q_full(w), (queries[w] - 1) & 1);
+          if (queries[w]) bar_wait(q_full(w), (queries[w] - 1) & 1);
         for (int i = 0; i < min(count, kStages); ++i)
-          if (!(held >> i & 1)) drain(full((count - 1 - i) % kStages), ((count - 1 - i) / kStages) & 1);
-        for (int i = max(0, lasts - 2); i < lasts; ++i) drain(v_last(i), (i >> 1) & 1);
+          if (!(held >> i & 1)) bar_wait(full((count - 1 - i) % kStages), ((count - 1 - i) / kStages) & 1);
+        for (int i = max(0, lasts - 2); i < lasts; ++i) bar_wait(v_last(i), (i >> 1) & 1);
       }
     } else {
       // ------------------------------------------ items and the last V tile
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!all(copied, k & 1)) break;
           if (lane == 0) {
             take_cta(smem_addr(s_taken), taken);
-            for (int i = 0; i < kPolls && !bar_try(taken, k & 1); ++i) {}
+            bar_wait(taken, k & 1);
           }
           __syncwarp();
           index = all(taken, k & 1) ? taken_cta(smem_addr(s_taken)) : -1;
@@ -449,7 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = all(s_full(w), (tiles + j) & 1);
         if (!ok) break;
         fence_after();
-        const int left = seen - (it.first + j) * kKeys; // keys of the tile that the row sees
+        // keys of the tile that the row sees; a row that is not used needs no
+        // mask (its weights reach nothing), and would cost its warp one
+        const int left = valid ? seen - (it.first + j) * kKeys : kKeys;
         const bool masked = __any_sync(0xffffffffu, left < kKeys);
         uint32_t s[kKeys];
         float m[4] = {ref, ref, ref, ref};
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the weights then stay below 2^8, and the accumulator in tensor
         // memory is rarely rescaled.  The product that reads it is done:
         // the scores of this tile were issued after it.
-        const bool move = (top - ref) * a.scale2 > 8.f || ref == -INFINITY;
+        const bool move = valid && ((top - ref) * a.scale2 > 8.f || ref == -INFINITY);
         if (__any_sync(0xffffffffu, move && j > 0 && top > ref)) {
           const float f = move && top > ref ? ex2((ref - top) * a.scale2) : 1.f;
           l *= f;

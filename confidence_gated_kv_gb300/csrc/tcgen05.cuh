@@ -22,15 +22,27 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// One poll of a phase (the hardware may let the thread sleep for a while).
+// One poll of a phase; the thread may sleep in it, for up to kSleepNs unless
+// the phase completes.  A poll that returns at once instead takes issue slots
+// from the softmax warps of the same quarter of the SM.
+constexpr uint32_t kSleepNs = 20000;
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kSleepNs)
       : "memory");
   return ok != 0;
+}
+// Polls until the phase completes; false after about four seconds.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  if (bar_try(bar, parity)) return true;
+  const long long start = clock64();
+  do {
+    if (bar_try(bar, parity)) return true;
+  } while (clock64() - start < (1LL << 33));
+  return false;
 }
 
 // Barrier ID over `threads` threads of converged warps.
