@@ -76,7 +76,11 @@ struct Item {                            // what one CTA computes
   int t0, head;                          // first token (within the sequence), KV head
   int first;                             // first key tile (of a split item)
   int n0, n1;                            // key tiles of each row tile, from `first` on
+  int dual;                              // one row tile for both warpgroups, which take every other key tile
 };
+
+// Key tiles of an item.
+__device__ __forceinline__ int key_tiles(const Item& it) { return it.dual ? it.n0 + it.n1 : max(it.n0, it.n1); }
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
@@ -117,8 +121,9 @@ __device__ bool find_item(const Args& a, int tile, int head, int rank, int split
         const int n0 = (seen0 + kKeys - 1) / kKeys, n1 = end > mid ? (seen1 + kKeys - 1) / kKeys : 0;
         const int n = max(n0, n1), from = n * rank / split, to = n * (rank + 1) / split;
         it->first = from;
-        it->n0 = clampi(n0 - from, 0, to - from);
-        it->n1 = clampi(n1 - from, 0, to - from);
+        it->dual = split > 1 && end == mid;
+        it->n0 = it->dual ? (to - from + 1) / 2 : clampi(n0 - from, 0, to - from);
+        it->n1 = it->dual ? (to - from) / 2 : clampi(n1 - from, 0, to - from);
       }
       return true;
     }
@@ -239,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one lane issues.
       constexpr uint32_t dqk = mma_desc(kRows, kKeys, BF16, false), dpv = mma_desc(kRows, D, BF16, true);
       const int w = warp == 11;
-      const uint32_t scores = tmem + w * kKeys, output = tmem + kOut + w * D, q = desc_lo(sq + w * kBytes, 16);
+      const uint32_t scores = tmem + w * kKeys, output = tmem + kOut + w * D;
+      uint32_t q = 0;
       auto issue_s = [&](int stage) {
         const uint32_t k = desc_lo(skv + stage * kBytes, 16);
 #pragma unroll
@@ -255,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kKeys / 16; ++i)
           mma_ts(output, scores + 8 * i, v + i * (2048 >> 4), desc_hi(1024), dpv, accumulate || i > 0);
+        mma_commit(empty(stage));
       };
       bool ok = true;
       int stage = -1;                                   // the latest tile of the ring and its parity
@@ -266,13 +273,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = ok && all(full(stage), parity);
       };
+      auto skip = [&](int tiles) {                      // tiles that only the other warp uses
+        for (int i = 0; i < 2 * tiles && ok; ++i) {
+          next_full();
+          if (ok && lane == 0) bar_arrive(empty(stage));
+        }
+      };
       uint32_t tiles = 0, items = 0;                    // done by this warp: parities of its barriers
       Item it;
       for (int k = 0; ok && get_item(k, it); ++k) {
-        const int nw = w ? it.n1 : it.n0, n = max(it.n0, it.n1);
+        const int nw = w ? it.n1 : it.n0;
+        const bool dual = SPLIT && it.dual;
+        const int wq = dual ? 0 : w;                    // the row tile
+        q = desc_lo(sq + wq * kBytes, 16);
+        int passed = 0;                                 // key tiles
         if (nw > 0) {
+          if (dual && w) {
+            skip(1);
+            passed = 1;
+          }
           next_full();
-          ok = ok && all(q_full(w), items & 1);
+          ok = ok && all(q_full(wq), items & 1);
           if (ok) {
             fence_after();
             if (elect()) {
@@ -285,26 +306,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < nw && ok; ++j) {
           next_full();                                  // V of this tile
           const int v = stage;
-          if (j + 1 < nw) next_full();                  // K of the next one
+          const bool more = j + 1 < nw;
+          ++passed;
+          if (more && !dual) next_full();               // K of the next one
           ok = ok && all(p_full(w), (tiles + j) & 1);
           if (!ok) break;
           fence_after();
           if (elect()) {
             issue_o(v, j > 0);
-            if (j + 1 < nw) {
+            if (!more) mma_commit(o_full(w));
+            if (more && !dual) {
               issue_s(stage);
               if (j + 2 == nw) mma_commit(q_empty(w));
-            } else {
-              mma_commit(o_full(w));
             }
-            mma_commit(empty(v));
           }
           __syncwarp();
+          if (more && dual) {
+            skip(1);
+            ++passed;
+            next_full();
+            if (ok && elect()) issue_s(stage);
+            __syncwarp();
+          }
         }
-        for (int i = 2 * nw; i < 2 * n && ok; ++i) {    // tiles that only the other row tile sees
-          next_full();
-          if (ok && lane == 0) bar_arrive(empty(stage));
-        }
+        skip(key_tiles(it) - passed);
         tiles += nw;
         items += nw > 0;
       }
@@ -321,11 +346,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Item it;
       for (int k = 0; ok && get_item(k, it); ++k) {
-        const int n = max(it.n0, it.n1);
+        const int n = key_tiles(it);
         const bool partial = (it.first + n) * kKeys > it.lk;     // the last tile ends behind the sequence
         if (lane == 0) {
           auto load_q = [&](int w) {
-            if ((w ? it.n1 : it.n0) == 0) return;
+            if ((w ? it.n1 : it.n0) == 0 || (w && it.dual)) return;
             uint32_t& used = w ? queries[1] : queries[0];
             if (used > 0) ok = ok && wait(q_empty(w), (used - 1) & 1);
             if (!ok) return;
@@ -382,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool more = it.found != 0;
       for (int k = 0; more; ++k) {
         const Item now = it;
-        const int n = max(now.n0, now.n1);
+        const int n = key_tiles(now);
         int index = -1;
         if (!SPLIT) {
           // Once the last copies of this item are issued: early enough for
@@ -438,8 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
     for (int k = 0; ok && get_item(k, it); ++k) {
       const int nw = w ? it.n1 : it.n0;                 // key tiles of this row tile
-      if (it.t0 + w * a.tokens >= it.lq) continue;
-      const int t = it.t0 + w * a.tokens + row / a.G;
+      const bool dual = SPLIT && it.dual;
+      const int t0 = it.t0 + (dual ? 0 : w) * a.tokens; // first token of the row tile
+      if (t0 >= it.lq) continue;
+      const int t = t0 + row / a.G;
       const bool valid = row < a.tokens * a.G && t < it.lq;
       const int seen = !valid ? 0 : a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
       ref = -INFINITY;                                  // reference of the exponentials, and their sum
@@ -450,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         // keys of the tile that the row sees; a row that is not used needs no
         // mask (its weights reach nothing), and would cost its warp one
-        const int left = valid ? seen - (it.first + j) * kKeys : kKeys;
+        const int left = valid ? seen - (it.first + (dual ? 2 * j + w : j)) * kKeys : kKeys;
         const bool masked = __any_sync(0xffffffffu, left < kKeys);
         uint32_t s[kKeys];
         float m[4] = {ref, ref, ref, ref};
@@ -572,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int w = warp >> 2, nw = w ? it.n1 : it.n0;
       sums[threadIdx.x] = make_float2(ref, l);
       const uint32_t to = tmem + kOut + w * D + ((uint32_t)(warp & 3) << 21);
-      const int rows = min(a.tokens, it.lq - it.t0 - w * a.tokens) * a.G;
+      const int rows = min(a.tokens, it.lq - it.t0 - (it.dual ? 0 : w) * a.tokens) * a.G;
       if ((warp & 3) * 32 < rows) {                     // warps with a row that is used
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
@@ -597,26 +624,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = rank + split * warp; i < rows; i += split * (kThreads / 32)) {
         const int slot = i < per ? i : kRows + i - per, t = it.t0 + i / a.G;
         const int seen = a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
-        Vec y[kMaxSplit];
-        float2 z[kMaxSplit];
-#pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)             // all parts in flight
-          if (r < split) {
-            y[r] = *reinterpret_cast<const Vec*>(cluster.map_shared_rank(part, r) + slot * T::kPitch + lane * kVec);
-            z[r] = *(cluster.map_shared_rank(sums, r) + slot);
-          }
+        // the row's parts: one of each CTA, or with two warpgroups per row two
         float top = -INFINITY, sum = 0.f, x[kVec] = {};
+        for (int at = slot; at < (it.dual ? 2 * kRows : slot + 1); at += kRows) {
+          Vec y[kMaxSplit];
+          float2 z[kMaxSplit];
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)
-          if (r < split) top = fmaxf(top, z[r].x);
+          for (int r = 0; r < kMaxSplit; ++r)           // all parts in flight
+            if (r < split) {
+              y[r] = *reinterpret_cast<const Vec*>(cluster.map_shared_rank(part, r) + at * T::kPitch + lane * kVec);
+              z[r] = *(cluster.map_shared_rank(sums, r) + at);
+            }
+          const float before = top;
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)
-          if (r < split) {
-            const float f = z[r].x == top ? 1.f : ex2((z[r].x - top) * a.scale2);
-            sum += z[r].y * f;
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < split) top = fmaxf(top, z[r].x);
+          const float old = before == top ? 1.f : ex2((before - top) * a.scale2);
+          sum *= old;
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) x[j] += reinterpret_cast<const float*>(&y[r])[j] * f;
-          }
+          for (int j = 0; j < kVec; ++j) x[j] *= old;
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < split) {
+              const float f = z[r].x == top ? 1.f : ex2((z[r].x - top) * a.scale2);
+              sum += z[r].y * f;
+#pragma unroll
+              for (int j = 0; j < kVec; ++j) x[j] += reinterpret_cast<const float*>(&y[r])[j] * f;
+            }
+        }
         const float inv = 1.f / sum;
         uint16_t* dst = a.out + (long long)(it.q0 + t) * a.out_token +
                         (long long)(it.head * a.G + i % a.G) * a.out_head + lane * kVec;
