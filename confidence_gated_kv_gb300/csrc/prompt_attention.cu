@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys of the tile that the row sees; a row that is not used needs no
         // mask (its weights reach nothing), and would cost its warp one
         const int left = valid ? seen - (it.first + (dual ? 2 * j + w : j)) * kKeys : kKeys;
-        const bool masked = __any_sync(0xffffffffu, left < kKeys);
+        const int least = __reduce_min_sync(0xffffffffu, left);   // what every row of the warp sees
         uint32_t s[kKeys];
         float m[4] = {ref, ref, ref, ref};
         tmem_ld32(ts, s);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) {           // the maximum of a quarter while the next one loads
           if (c + 32 < kKeys) tmem_ld32(ts + c + 32, s + c + 32);
-          if (masked) {
+          if (least < c + 32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (c + i >= left) s[c + i] = 0xff800000u;
