@@ -41,6 +41,7 @@ constexpr int kKeys = 128;               // keys per tile
 constexpr int kThreads = 384;            // two softmax warpgroups, one for copies and products
 
 constexpr int kRegs = 168;               // registers a thread at launch: 65536 / 384, in eights
+constexpr int kSMs = 152;
 constexpr int kMaxSplit = 8;             // CTAs of a cluster that share an item
 
 template <int D, bool SPLIT>
@@ -753,23 +754,40 @@ int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, 
                      : launch<D, BF16, false>(mq, mk, mv, a, items, st);
 }
 
-// CTAs that share an item's keys, from what the host knows: the largest
-// number of items and the average number of key tiles of a sequence.  Time is
-// taken as rounds of the SMs times (tiles of a CTA + the tiles that its start
-// and its merge cost).
-int choose_split(long long items, double tiles) {
-  if (items >= 4LL * 152) return 1;
-  int best = 1;
+// How the items are launched, from what the host knows: the largest number of
+// items and the average number of key tiles of a sequence.  Time is taken as
+// rounds of the SMs times (key tiles of a CTA + the tiles that its start and
+// its merge take).  A last round with few items can go into a launch of its
+// own whose keys are split (160 items of 117 tiles: 323 us with all of them
+// split in two, 251 us as 152 whole ones and 8 split in eight).
+struct Plan {
+  long long whole, rest;                 // items of the first launch, and of one more
+  int split, rest_split;
+};
+
+double rounds_cost(long long items, double tiles, int* split) {
   double least = 1e30;
   for (int s = 1; s <= kMaxSplit; s *= 2) {
-    const double rounds = std::max(1.0, (double)items * s / 152.0);
-    const double t = (s == 1 ? std::ceil(rounds) : rounds) * (std::ceil(tiles / s) + (s == 1 ? 3.0 : 4.0));
+    const double t = std::ceil((double)items * s / kSMs) * (std::ceil(tiles / s) + (s == 1 ? 3.0 : 4.0));
     if (t < least) {
       least = t;
-      best = s;
+      *split = s;
     }
   }
-  return best;
+  return least;
+}
+
+Plan plan_items(long long items, double tiles) {
+  Plan p{items, 0, 1, 1};
+  if (items >= 4LL * kSMs) return p;     // enough rounds to even out
+  const double one = rounds_cost(items, tiles, &p.split);
+  const long long whole = items / kSMs * kSMs;
+  if (whole > 0 && whole < items) {
+    int split = 1;
+    const double two = whole / kSMs * (tiles + 3.0) + rounds_cost(items - whole, tiles, &split) + 2.0;
+    if (two < one) p = Plan{whole, items - whole, 1, split};
+  }
+  return p;
 }
 
 bool rows_ok(const void* p, const int64_t* stride, int d, long long tokens, long long heads) {
@@ -813,9 +831,9 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
   a.scale = p->scale;
   a.scale2 = p->scale * 1.4426950408889634f;
   // no more tiles than these, whatever the lengths
-  const long long tiles = (long long)p->total_q / (2 * a.tokens) + p->B;
+  const int per = 2 * a.tokens;
+  const long long tiles = p->B == 1 ? (p->total_q + per - 1LL) / per : (long long)p->total_q / per + p->B;
   if (tiles * p->Hkv >= (1LL << 31) / kMaxSplit) return CONFKV_EINVAL;
-  a.split = choose_split(tiles * p->Hkv, (double)p->total_k / p->B / kKeys);
   a.wide = reinterpret_cast<uintptr_t>(p->out) % 32 == 0 && (p->total_q < 2 || p->out_stride[0] % 16 == 0) &&
            (p->Hq < 2 || p->out_stride[1] % 16 == 0);
   const bool bf16 = p->dtype == CONFKV_Q_BF16;
@@ -832,11 +850,15 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
   const int r = status_word(&a.status);
   if (r != CONFKV_OK) return r;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (p->d == 128)
-    return bf16 ? launch<128, true>(mq, mk, mv, a, tiles * p->Hkv, st)
-                : launch<128, false>(mq, mk, mv, a, tiles * p->Hkv, st);
-  return bf16 ? launch<64, true>(mq, mk, mv, a, tiles * p->Hkv, st)
-              : launch<64, false>(mq, mk, mv, a, tiles * p->Hkv, st);
+  const Plan plan = plan_items(tiles * p->Hkv, (double)p->total_k / p->B / kKeys);
+  auto fn = p->d == 128 ? (bf16 ? launch<128, true> : launch<128, false>)
+                        : (bf16 ? launch<64, true> : launch<64, false>);
+  a.split = plan.split;
+  const int first = fn(mq, mk, mv, a, plan.whole, st);
+  if (first != CONFKV_OK || plan.rest == 0) return first;
+  a.item0 = (int)plan.whole;
+  a.split = plan.rest_split;
+  return fn(mq, mk, mv, a, plan.rest, st);
 }
 
 extern "C" int confkv_prompt_status(int32_t* bits, void* stream) {

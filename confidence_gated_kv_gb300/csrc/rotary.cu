@@ -134,7 +134,7 @@ __device__ __forceinline__ void angle(const RotArgs& a, int pos, int i, float* c
 // threads take a row each, two 8-channel chunks per thread, with the next
 // row in flight.  (One thread computing its own angles for four heads, without
 // shared memory, was bound by instructions: 49 us for 8192 tokens of 48
-// heads of 128 channels against ROTARY_US now.)
+// heads of 128 channels against 45 now.)
 constexpr int kMaxTokens = 16;
 template <int TPR, int IN>
 __global__ void __launch_bounds__(256, 3) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
