@@ -36,13 +36,15 @@ constexpr int kReadWarps = 8;
 
 // ------------------------------------------------------------------ reset
 
-__global__ void prefill_reset_kernel(Shape s, Dev d, LengthChunk c) {
+__global__ void prefill_reset_kernel(Shape s, Dev d, const __grid_constant__ LengthChunk c) {
+  pdl_wait();
   for (int i = threadIdx.x; i < c.count; i += blockDim.x) {
     d.T0[c.first + i] = c.len[i];
     d.conf_done[c.first + i] = 0;
     d.conf_ready[c.first + i] = 0;
-    for (int l = 0; l < s.L; ++l) d.arrive[(size_t)l * s.B + c.first + i] = 0;
   }
+  for (int i = threadIdx.x; i < c.count * s.L; i += blockDim.x)
+    d.arrive[(size_t)(i / c.count) * s.B + c.first + i % c.count] = 0;
   if (threadIdx.x == 0) {            // packed row of each sequence
     long long row = c.row0;
     for (int i = 0; i < c.count; ++i) {
@@ -507,10 +509,10 @@ int launch_prefill_reset(const Shape& s, const Dev& d, const int32_t* len, cudaS
   for (c.first = 0; c.first < s.B; c.first += LengthChunk::kMax) {
     c.count = std::min(LengthChunk::kMax, s.B - c.first);
     for (int i = 0; i < c.count; ++i) c.len[i] = len[c.first + i];
-    prefill_reset_kernel<<<1, 256, 0, st>>>(s, d, c);
+    if (launch_pdl(prefill_reset_kernel, dim3(1), dim3(256), 0, st, s, d, c) != cudaSuccess) return -1;
     for (int i = 0; i < c.count; ++i) c.row0 += c.len[i];
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return 0;
 }
 
 template <int D, bool BF16>

@@ -207,7 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&map_k);
     tma_prefetch_map(&map_v);
   }
-  // what the CTA starts with, while the barriers are set up
+  // what the CTA starts with, while the barriers are set up; nothing before
+  // this point touches memory that the previous kernel may write
+  pdl_wait();
   const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0;
   if (warp == 10) {
     const int index = a.item0 + blockIdx.x / split;     // an item per CTA, or per cluster
@@ -738,12 +740,14 @@ int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = a.split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = a.split;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = SPLIT ? 1 : 0;
+  cfg.numAttrs = SPLIT ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a) == cudaSuccess ? CONFKV_OK : CONFKV_ECUDA;
 }
 

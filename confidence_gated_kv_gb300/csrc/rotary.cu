@@ -139,6 +139,7 @@ constexpr int kMaxTokens = 16;
 template <int TPR, int IN>
 __global__ void __launch_bounds__(256, 3) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
   constexpr int kGroups = 256 / TPR;
+  pdl_wait();
   extern __shared__ __align__(16) float s_turn[];        // [token][cosines, sines][rot / 2]
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int heads = a.Hq + a.Hkv;
@@ -318,9 +319,10 @@ void launch_rows(RotArgs a, cudaStream_t st) {
   a.heads = (heads + parts - 1) / parts;
   const dim3 grid((unsigned)blocks, (unsigned)((heads + a.heads - 1) / a.heads));
   const size_t smem = (size_t)a.tokens * a.rot * sizeof(float);
-  if (a.in_type == CONFKV_FP32) rotary_rows_kernel<TPR, CONFKV_FP32><<<grid, 256, smem, st>>>(a);
-  else if (a.in_type == CONFKV_BF16) rotary_rows_kernel<TPR, CONFKV_BF16><<<grid, 256, smem, st>>>(a);
-  else rotary_rows_kernel<TPR, CONFKV_FP16><<<grid, 256, smem, st>>>(a);
+  auto kernel = a.in_type == CONFKV_FP32   ? rotary_rows_kernel<TPR, CONFKV_FP32>
+                : a.in_type == CONFKV_BF16 ? rotary_rows_kernel<TPR, CONFKV_BF16>
+                                           : rotary_rows_kernel<TPR, CONFKV_FP16>;
+  launch_pdl(kernel, grid, dim3(256), smem, st, a);
 }
 
 }  // namespace

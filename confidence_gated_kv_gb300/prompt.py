@@ -17,14 +17,13 @@ _ROTARY = struct.Struct("=10i2f4Q8q4Q")
 _PROMPT = struct.Struct("=8if4x7Q8q")
 
 
-def _int32():
-    import torch
-    return torch.int32
+torch = None      # bound by the first call: importing the package does not load torch
 
 
-def _new(shape, device):
-    import torch
-    return torch.empty(shape, dtype=torch.float32, device=device)
+def _bind():
+    global torch
+    import torch as t
+    torch = t
 
 
 class Rotary:
@@ -36,7 +35,8 @@ class Rotary:
     def __init__(self, rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                  original_length: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
                  interleaved: bool = False, device=None):
-        import torch
+        if torch is None:
+            _bind()
         if scaling not in SCALINGS:
             raise ValueError("scaling is one of %s" % ", ".join(SCALINGS))
         self.rot_dim, self.interleaved = int(rot_dim), int(bool(interleaved))
@@ -80,7 +80,6 @@ def _vector(t, name, n, dtype, dev):
 
 def _like(t):
     """New contiguous tensor of the shape, type and device of t."""
-    import torch
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
@@ -98,6 +97,8 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
     None (norms only), k None (queries only).  Returns (q_out, k_out): new
     tensors of the inputs' type, or the given ones, which may be of another
     type, strided, or the inputs themselves."""
+    if torch is None:
+        _bind()
     (n, Hq, d), qs = _dims(q, "q")
     dev, code = q.get_device(), dtype_code(q.dtype)
     if q_out is None:
@@ -133,7 +134,7 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
         rot, interleaved, mscale, turns_at = rotary.rot_dim, rotary.interleaved, rotary.mscale, rotary.turns_at
         if positions is None or rotary.device_index != dev:
             _unfit("positions, and a rotary table on the device of q, are wanted")
-        pos_at = _vector(positions, "positions", n, _int32(), dev)
+        pos_at = _vector(positions, "positions", n, torch.int32, dev)
     args = _ROTARY.pack(n, Hq, Hkv, d, rot, interleaved, code, w_code, qo_code, ko_code, eps, mscale, q.data_ptr(),
                         k_at, q_out.data_ptr(), ko_at, qs[0], qs[1], ks[0], ks[1], qos[0], qos[1], kos[0], kos[1],
                         qw_at, kw_at, pos_at, turns_at)
@@ -149,6 +150,8 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     same for keys (default: cu_seqlens).  With `causal` the queries are the
     last of their sequence's keys.  scale defaults to 1 / sqrt(d).  Returns
     out, or (out, lse) with return_lse; lse is fp32 [rows, Hq]."""
+    if torch is None:
+        _bind()
     (nq, Hq, d), qs = _dims(q, "q")
     dev, dtype = q.get_device(), q.dtype
     (nk, Hkv, dk), ks = _dims(k, "k", dev)
@@ -156,9 +159,9 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     if shape != k.shape or dk != d or k.dtype != dtype or v.dtype != dtype:
         _unfit("k and v: one shape, and the channels and type of q, are wanted")
     B = len(cu_seqlens) - 1
-    cu_at = cuk_at = _vector(cu_seqlens, "cu_seqlens", B + 1, _int32(), dev)
+    cu_at = cuk_at = _vector(cu_seqlens, "cu_seqlens", B + 1, torch.int32, dev)
     if cu_seqlens_k is not None:
-        cuk_at = _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, _int32(), dev)
+        cuk_at = _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, torch.int32, dev)
     if out is None:
         out, os = _like(q), (Hq * d, d)
     else:
@@ -171,7 +174,7 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
             _unfit("lse: a contiguous fp32 [rows, heads] tensor on the device of q is wanted")
         lse_at = lse.data_ptr()
     elif return_lse:
-        lse = _new((nq, Hq), q.device)
+        lse = torch.empty((nq, Hq), dtype=torch.float32, device=q.device)
         lse_at = lse.data_ptr()
     args = _PROMPT.pack(B, Hq, Hkv, d, dtype_code(dtype), 1 if causal else 0, nq, nk,
                         d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
