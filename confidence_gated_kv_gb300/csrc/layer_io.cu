@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kReadWarps * 32, 4)
   __shared__ __align__(16) uint8_t s_blk[kReadWarps][32 * kPitch];   // 16 rows of bytes, or of halves
   __shared__ int s_count[kCountHere];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x / spans, h = unit % s.Hkv, b = unit / s.Hkv;
+  // K or V of one (sequence, KV head)
+  const int unit = blockIdx.x / spans >> 1, kv = blockIdx.x / spans & 1, h = unit % s.Hkv, b = unit / s.Hkv;
   const int ch = lane % kPer, g = lane >> 2, t = lane & 3;
   pdl_wait();
   const size_t lb = lb_index(s, layer, b), u = unit_index(s, layer, b, h);
@@ -387,117 +388,128 @@ __global__ void __launch_bounds__(kReadWarps * 32, 4)
   }
   const int n8 = d.n8[lb], nb8 = (n8 + 15) / 16, nb = nb8 + s.WR / 16;
   const int32_t* pos = d.pos + lb * s.S;
+  const bool first = h == 0 && kv == 0;                // writes the positions
   uint8_t* blk = s_blk[warp];
-  const int i0 = ((blockIdx.x % spans) * kReadWarps + warp) * per_warp;
-  for (int i = i0; i < min(i0 + per_warp, nb); ++i) {
-    const bool ring = i >= nb8;
-    // output row of slot `lane` (lanes 0-15); -1: nothing there
-    int row = -1, p = -1;
-    if (!ring) {
-      const int slot = i * 16 + lane;
-      if (lane < 16 && slot < n8) {
-        row = row0 + slot;
-        p = pos[slot];
-      }
-    } else {                                           // by position: behind the older entries of the ring
-      const int32_t* rp = pos + s.cap;
-      p = lane < 16 ? rp[(i - nb8) * 16 + lane] : -1;
-      int older[16] = {};
-      for (int j = lane; j < s.WR; j += 32) {
-        const int x = rp[j];
+  uint16_t* out = (kv ? v + h * v_h : k + h * k_h) + ch * 8;
+  const long long ot = kv ? v_t : k_t;
+  const int i0 = ((blockIdx.x % spans) * kReadWarps + warp) * per_warp, i1 = min(i0 + per_warp, nb);
+
+  // ---- INT8 blocks, the next one in flight
+  if (i0 < nb8) {
+    float scale[8];
+    const float4* sc = reinterpret_cast<const float4*>((kv ? d.sV : d.sK) + u * D + ch * 8);
+    const float4 s0 = sc[0], s1 = sc[1];
+    scale[0] = s0.x; scale[1] = s0.y; scale[2] = s0.z; scale[3] = s0.w;
+    scale[4] = s1.x; scale[5] = s1.y; scale[6] = s1.z; scale[7] = s1.w;
+    const uint8_t* src = (kv ? d.v8 : d.k8) + (u * (s.cstride / 16) + i0) * 16 * D + lane * 16;
+    uint4 next[D / 32];
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          older[q] += x >= 0 && x < rp[(i - nb8) * 16 + q];
-      }
+    for (int r = 0; r < D / 32; ++r) next[r] = *reinterpret_cast<const uint4*>(src + r * 512);
+    for (int i = i0; i < min(i1, nb8); ++i) {
+      uint4 x[D / 32];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int n = __reduce_add_sync(0xffffffffu, older[q]);
-        if (lane == q && p >= 0) row = row0 + n8 + n;
+      for (int r = 0; r < D / 32; ++r) x[r] = next[r];
+      src += 16 * D;
+      if (i + 1 < min(i1, nb8)) {
+#pragma unroll
+        for (int r = 0; r < D / 32; ++r) next[r] = *reinterpret_cast<const uint4*>(src + r * 512);
       }
+      if (kv) {                                        // v8_offset: channel 8 (4 r + j) + g, four tokens
+#pragma unroll
+        for (int r = 0; r < D / 32; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = (&x[r].x)[j];
+            uint8_t* o = blk + (4 * r + j) * 8 + g;
+            o[(2 * t) * kPitch] = (uint8_t)w;
+            o[(2 * t + 1) * kPitch] = (uint8_t)(w >> 8);
+            o[(2 * t + 8) * kPitch] = (uint8_t)(w >> 16);
+            o[(2 * t + 9) * kPitch] = (uint8_t)(w >> 24);
+          }
+      } else {                                         // k8_offset: token 8 nt + g, two channel pairs
+#pragma unroll
+        for (int r = 0; r < D / 32; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = (&x[r].x)[j];
+            const int nt = r / (D / 64), kk = (r % (D / 64)) * 4 + j;
+            uint8_t* o = blk + (8 * nt + g) * kPitch + 16 * kk + 2 * t;
+            *reinterpret_cast<uint16_t*>(o) = (uint16_t)w;
+            *reinterpret_cast<uint16_t*>(o + 8) = (uint16_t)(w >> 16);
+          }
+      }
+      __syncwarp();
+      const int tokens = min(16, n8 - i * 16), row = row0 + i * 16;   // entries of the block and their first row
+      if (row + tokens > rows && lane == 0) atomicOr(d.status, kStatusCapacity);
+      const int fit = min(tokens, rows - row);
+      if (first && lane < fit) positions[row + lane] = pos[i * 16 + lane];
+#pragma unroll
+      for (int r = 0; r < 16; r += kRowsAtOnce) {
+        const int tau = r + lane / kPer;
+        const uint4 y = dequantise(*reinterpret_cast<const uint2*>(blk + tau * kPitch + ch * 8), scale, BF16);
+        if (tau < fit) *reinterpret_cast<uint4*>(out + (row + tau) * ot) = y;
+      }
+      __syncwarp();
+    }
+  }
+
+  // ---- blocks of the window
+  for (int i = max(i0, nb8); i < i1; ++i) {
+    // output row of slot `lane` (lanes 0-15): behind the ring's older entries; -1: nothing there
+    const int32_t* rp = pos + s.cap;
+    const int p = lane < 16 ? rp[(i - nb8) * 16 + lane] : -1;
+    int row = -1, older[16] = {};
+    for (int j = lane; j < s.WR; j += 32) {
+      const int x = rp[j];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) older[q] += x >= 0 && x < rp[(i - nb8) * 16 + q];
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int n = __reduce_add_sync(0xffffffffu, older[q]);
+      if (lane == q && p >= 0) row = row0 + n8 + n;
     }
     if (row >= rows) {
       atomicOr(d.status, kStatusCapacity);
       row = -1;
     }
-    if (h == 0 && row >= 0) positions[row] = p;
-    const uint8_t* code[2] = {d.k8 + (u * (s.cstride / 16) + i) * 16 * D, d.v8 + (u * (s.cstride / 16) + i) * 16 * D};
+    if (first && row >= 0) positions[row] = p;
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(kv ? d.v16 : d.k16) + (u * (s.WR / 16) + (i - nb8)) * 32 * D;
+    uint16_t* half = reinterpret_cast<uint16_t*>(blk);
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      float scale[8];
-      if (!ring) {
-        const float4* sc = reinterpret_cast<const float4*>((kv ? d.sV : d.sK) + u * D + ch * 8);
-        const float4 s0 = sc[0], s1 = sc[1];
-        scale[0] = s0.x; scale[1] = s0.y; scale[2] = s0.z; scale[3] = s0.w;
-        scale[4] = s1.x; scale[5] = s1.y; scale[6] = s1.z; scale[7] = s1.w;
-        uint4 x[D / 32];
+    for (int r = 0; r < D / 16; ++r) {
+      const uint4 y = *reinterpret_cast<const uint4*>(src + r * 512 + lane * 16);
 #pragma unroll
-        for (int r = 0; r < D / 32; ++r) x[r] = *reinterpret_cast<const uint4*>(code[kv] + r * 512 + lane * 16);
-#pragma unroll
-        for (int r = 0; r < D / 32; ++r) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t w = (&x[r].x)[j];
-            if (kv) {                                  // v8_offset: channel 8 (4 r + j) + g, four tokens
-              uint8_t* o = blk + (4 * r + j) * 8 + g;
-              o[(2 * t) * kPitch] = (uint8_t)w;
-              o[(2 * t + 1) * kPitch] = (uint8_t)(w >> 8);
-              o[(2 * t + 8) * kPitch] = (uint8_t)(w >> 16);
-              o[(2 * t + 9) * kPitch] = (uint8_t)(w >> 24);
-            } else {                                   // k8_offset: token 8 nt + g, two channel pairs
-              const int nt = r / (D / 64), kk = (r % (D / 64)) * 4 + j;
-              uint8_t* o = blk + (8 * nt + g) * kPitch + 16 * kk + 2 * t;
-              *reinterpret_cast<uint16_t*>(o) = (uint16_t)w;
-              *reinterpret_cast<uint16_t*>(o + 8) = (uint16_t)(w >> 16);
-            }
-          }
-        }
-      } else {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(kv ? d.v16 : d.k16) +
-                             (u * (s.WR / 16) + (i - nb8)) * 32 * D;
-        uint16_t* half = reinterpret_cast<uint16_t*>(blk);
-#pragma unroll
-        for (int r = 0; r < D / 16; ++r) {
-          const uint4 y = *reinterpret_cast<const uint4*>(src + r * 512 + lane * 16);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t w = (&y.x)[j];
-            if (kv) {                                  // v16_offset: channel 8 (2 r + j / 2) + g, two tokens
-              const int c = 8 * (2 * r + (j >> 1)) + g, tau = 8 * (j & 1) + 2 * t;
-              half[tau * kPitch + c] = (uint16_t)w;
-              half[(tau + 1) * kPitch + c] = (uint16_t)(w >> 16);
-            } else {                                   // k16_offset: token 8 nt + g, a channel pair
-              const int nt = r / (D / 32), kk = 2 * (r % (D / 32)) + (j >> 1);
-              *reinterpret_cast<uint32_t*>(half + (8 * nt + g) * kPitch + 16 * kk + 8 * (j & 1) + 2 * t) = w;
-            }
-          }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = (&y.x)[j];
+        if (kv) {                                      // v16_offset: channel 8 (2 r + j / 2) + g, two tokens
+          const int c = 8 * (2 * r + (j >> 1)) + g, tau = 8 * (j & 1) + 2 * t;
+          half[tau * kPitch + c] = (uint16_t)w;
+          half[(tau + 1) * kPitch + c] = (uint16_t)(w >> 16);
+        } else {                                       // k16_offset: token 8 nt + g, a channel pair
+          const int nt = r / (D / 32), kk = 2 * (r % (D / 32)) + (j >> 1);
+          *reinterpret_cast<uint32_t*>(half + (8 * nt + g) * kPitch + 16 * kk + 8 * (j & 1) + 2 * t) = w;
         }
       }
-      __syncwarp();
-      uint16_t* out = (kv ? v : k) + h * (kv ? v_h : k_h) + ch * 8;
-      const long long ot = kv ? v_t : k_t;
-#pragma unroll
-      for (int r = 0; r < 16; r += kRowsAtOnce) {
-        const int tau = r + lane / kPer;
-        const int to = __shfl_sync(0xffffffffu, row, tau);
-        uint4 y;
-        if (!ring) {
-          y = dequantise(*reinterpret_cast<const uint2*>(blk + tau * kPitch + ch * 8), scale, BF16);
-        } else {
-          y = *reinterpret_cast<const uint4*>(blk + (tau * kPitch + ch * 8) * 2);
-          if (BF16) {
-            uint32_t* w = &y.x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-              const __nv_bfloat162 q = __floats2bfloat162_rn(f.x, f.y);
-              w[j] = *reinterpret_cast<const uint32_t*>(&q);
-            }
-          }
-        }
-        if (to >= 0) *reinterpret_cast<uint4*>(out + to * ot) = y;
-      }
-      __syncwarp();
     }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 16; r += kRowsAtOnce) {
+      const int tau = r + lane / kPer;
+      const int to = __shfl_sync(0xffffffffu, row, tau);
+      uint4 y = *reinterpret_cast<const uint4*>(blk + (tau * kPitch + ch * 8) * 2);
+      if (BF16) {
+        uint32_t* w = &y.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          const __nv_bfloat162 q = __floats2bfloat162_rn(f.x, f.y);
+          w[j] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+      }
+      if (to >= 0) *reinterpret_cast<uint4*>(out + to * ot) = y;
+    }
+    __syncwarp();
   }
 }
 
@@ -558,9 +570,9 @@ int launch_read_layer(const Shape& s, const Dev& d, int layer, bool bf16, void* 
                       cudaStream_t st) {
   const bool counted = s.B > kCountHere;
   if (counted) count_entries_kernel<<<1, 1024, 0, st>>>(s, d, layer, cu);
-  // one block per warp until the GPU is full, then up to four
-  const long long blocks = (n8_bound + 15) / 16 + s.WR / 16, units = (long long)s.B * s.Hkv;
-  const long long per_warp = std::min(4LL, std::max(1LL, blocks * units / (152LL * 6 * kReadWarps)));
+  // one block per warp until the GPU is full, then up to eight
+  const long long blocks = (n8_bound + 15) / 16 + s.WR / 16, units = 2LL * s.B * s.Hkv;
+  const long long per_warp = std::min(8LL, std::max(1LL, blocks * units / (152LL * 8 * kReadWarps)));
   const int spans = (int)((blocks + kReadWarps * per_warp - 1) / (kReadWarps * per_warp));
   const dim3 grid((unsigned)(spans * units));
   auto kernel = s.D == 128 ? (bf16 ? read_layer_kernel<128, true> : read_layer_kernel<128, false>)

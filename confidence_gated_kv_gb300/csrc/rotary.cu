@@ -84,23 +84,6 @@ struct Raw {
     }
   }
 };
-__device__ __forceinline__ void load8(const void* p, long long i, int type, float* x) {
-  if (type == CONFKV_FP32) {
-    Raw<CONFKV_FP32> r;
-    r.load(p, i);
-    r.floats(x);
-  } else {
-    Raw<CONFKV_FP16> r;
-    r.load(p, i);
-    if (type == CONFKV_FP16) {
-      r.floats(x);
-    } else {
-      Raw<CONFKV_BF16> t;
-      t.w[0] = r.w[0];
-      t.floats(x);
-    }
-  }
-}
 __device__ __forceinline__ void store8(void* p, long long i, int type, const float* x) {
   if (type == CONFKV_FP32) {
     float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
@@ -134,13 +117,16 @@ __device__ __forceinline__ void angle(const RotArgs& a, int pos, int i, float* c
 // threads take a row each, two 8-channel chunks per thread, with the next
 // row in flight.  (One thread computing its own angles for four heads, without
 // shared memory, was bound by instructions: 49 us for 8192 tokens of 48
-// heads of 128 channels against 45 now.)
+// heads of 128 channels against 38 now.)
 constexpr int kMaxTokens = 16;
 template <int TPR, int IN>
-__global__ void __launch_bounds__(256, 3) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
-  constexpr int kGroups = 256 / TPR;
+__global__ void __launch_bounds__(256, 4) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
+  constexpr int kGroups = 256 / TPR, kDim = 16 * TPR;
   pdl_wait();
-  extern __shared__ __align__(16) float s_turn[];        // [token][cosines, sines][rot / 2]
+  // In the order in which the threads of a row read them, four floats each:
+  // weights of q and k, then [token][cosines, sines][rot / 2].
+  extern __shared__ __align__(16) float s_float[];
+  float* s_turn = s_float + 2 * kDim;
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int heads = a.Hq + a.Hkv;
   const int token0 = blockIdx.x * a.tokens, tokens = min(a.tokens, a.n - token0);
@@ -155,25 +141,45 @@ __global__ void __launch_bounds__(256, 3) rotary_rows_kernel(const __grid_consta
     c0 = t;
     c1 = t + half;
   }
-  auto fetch = [&](int r, Raw<IN>& r0, Raw<IN>& r1) {
-    const long long token = token0 + r / count;
-    const int head = head0 + r % count;
+  // rows group, group + kGroups, ... as (token, head of the block's)
+  struct Row {
+    int token, head;
+  };
+  const int dt = kGroups / count, dh = kGroups % count;
+  auto next = [&](Row& r) {
+    r.token += dt;
+    r.head += dh;
+    if (r.head >= count) {
+      r.head -= count;
+      ++r.token;
+    }
+  };
+  auto fetch = [&](const Row& r, Raw<IN>& r0, Raw<IN>& r1) {
+    const long long token = token0 + r.token;
+    const int head = head0 + r.head;
     const char* src = static_cast<const char*>(head < a.Hq ? a.q : a.k);
     const long long off = head < a.Hq ? token * a.q_t + head * a.q_h : token * a.k_t + (head - a.Hq) * a.k_h;
     r0.load(src, off + 8 * c0);
     r1.load(src, off + 8 * c1);
   };
   Raw<IN> r0 = {}, r1 = {};
-  if (group < rows) fetch(group, r0, r1);
+  Row row{group / count, group % count};
+  if (row.token < tokens) fetch(row, r0, r1);
+  for (int i = threadIdx.x; i < 2 * kDim; i += 256) {
+    const void* weight = i < kDim ? a.qw : a.kw;
+    const int c = i % kDim;
+    if (weight) s_float[i - c + (c >> 2 & 1) * (kDim / 2) + (c >> 3) * 4 + (c & 3)] = load1(weight, c, a.w_type);
+  }
   for (int i = threadIdx.x; i < tokens * pairs; i += 256) {
     const int token = i / pairs, p = i % pairs;
-    angle(a, a.pos[token0 + token], p, &s_turn[token * a.rot + p], &s_turn[token * a.rot + pairs + p]);
+    float* turn = s_turn + token * a.rot + (p >> 2 & 1) * (pairs / 2) + (p >> 3) * 4 + (p & 3);
+    angle(a, a.pos[token0 + token], p, turn, turn + pairs);
   }
   __syncthreads();
   for (int base = 0; base < rows; base += kGroups) {       // the same count for every thread
-    const int r = base + group;
-    const bool on = r < rows;
-    const int token = on ? r / count : 0, head = head0 + (on ? r % count : 0);
+    const Row now = row;
+    const bool on = now.token < tokens;
+    const int token = on ? now.token : 0, head = head0 + now.head;
     const bool is_q = head < a.Hq;
     Pair x[8];                                             // chunk c0, then c1
     {
@@ -183,7 +189,8 @@ __global__ void __launch_bounds__(256, 3) rotary_rows_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = Pair(f[2 * i], f[2 * i + 1]);
     }
-    if (r + kGroups < rows) fetch(r + kGroups, r0, r1);
+    next(row);
+    if (row.token < tokens) fetch(row, r0, r1);
     if (a.qw || a.kw) {
       Pair sq = x[0] * x[0];
 #pragma unroll
@@ -191,20 +198,21 @@ __global__ void __launch_bounds__(256, 3) rotary_rows_kernel(const __grid_consta
       float ss = sq.get().x + sq.get().y;
 #pragma unroll
       for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const void* weight = is_q ? a.qw : a.kw;
-      if (weight) {
-        const float f = rsqrtf(ss * (1.f / (16 * TPR)) + a.eps);
-        float g[16];
-        load8(weight, 8 * c0, a.w_type, g);
-        load8(weight, 8 * c1, a.w_type, g + 8);
+      if (is_q ? a.qw != nullptr : a.kw != nullptr) {
+        const float f = rsqrtf(ss * (1.f / kDim) + a.eps);
+        const float4* w = reinterpret_cast<const float4*>(s_float + (is_q ? 0 : kDim));
+        const float4 g[4] = {w[c0], w[kDim / 8 + c0], w[c1], w[kDim / 8 + c1]};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * Pair(f, f) * Pair(g[2 * i], g[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = x[2 * i] * Pair(f, f) * Pair(g[i].x, g[i].y);
+          x[2 * i + 1] = x[2 * i + 1] * Pair(f, f) * Pair(g[i].z, g[i].w);
+        }
       }
     }
     if (!on) continue;
     if (turned) {
-      const float4* turn = reinterpret_cast<const float4*>(s_turn + token * a.rot + 8 * t);
-      const float4 ca = turn[0], cb = turn[1], sa = turn[pairs / 4], sb = turn[pairs / 4 + 1];
+      const float4* turn = reinterpret_cast<const float4*>(s_turn + token * a.rot) + t;
+      const float4 ca = turn[0], cb = turn[half], sa = turn[2 * half], sb = turn[3 * half];
       const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
       const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
       if (a.interleaved) {
@@ -318,7 +326,7 @@ void launch_rows(RotArgs a, cudaStream_t st) {
   const int parts = (int)std::max<long long>(1, std::min<long long>((heads + groups - 1) / groups, 304 / blocks));
   a.heads = (heads + parts - 1) / parts;
   const dim3 grid((unsigned)blocks, (unsigned)((heads + a.heads - 1) / a.heads));
-  const size_t smem = (size_t)a.tokens * a.rot * sizeof(float);
+  const size_t smem = ((size_t)a.tokens * a.rot + 2 * 16 * TPR) * sizeof(float);
   auto kernel = a.in_type == CONFKV_FP32   ? rotary_rows_kernel<TPR, CONFKV_FP32>
                 : a.in_type == CONFKV_BF16 ? rotary_rows_kernel<TPR, CONFKV_BF16>
                                            : rotary_rows_kernel<TPR, CONFKV_FP16>;

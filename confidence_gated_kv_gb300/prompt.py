@@ -45,12 +45,16 @@ class Rotary:
         _check(lib().confkv_rotary_frequencies(self.rot_dim, float(base), SCALINGS[scaling], float(factor),
                                                float(original_length), float(beta_fast), float(beta_slow), host,
                                                ctypes.byref(mscale)), "confkv_rotary_frequencies")
-        self.mscale = float(mscale.value)
-        self.turns_host = [int(x) for x in host][:self.rot_dim // 2]
-        signed = [x - (1 << 64) if x >= 1 << 63 else x for x in self.turns_host]
+        self.mscale, self._host = mscale.value, host
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        self.turns = torch.tensor(signed, dtype=torch.int64, device=dev)
+        self.turns = torch.frombuffer(host, dtype=torch.int64).to(dev)
         self.turns_at, self.device_index = self.turns.data_ptr(), self.turns.get_device()
+
+
+    @property
+    def turns_host(self):
+        """Turns of each pair per position, in units of 2^-64."""
+        return list(self._host)[:self.rot_dim // 2]
 
 
 def _unfit(what):
