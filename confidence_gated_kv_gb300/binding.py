@@ -192,6 +192,15 @@ def on_device(index: int):
     return _same if index == _current_device() else torch.cuda.device(index)
 
 
+def allocating_on(stream):
+    """Context for new tensors that work on `stream` (None: the current one)
+    will write: memory of the current stream may still be in use there."""
+    if stream is None:
+        return _same
+    import torch
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
 _raw_stream_fn = None
 
 
@@ -351,10 +360,11 @@ class Cache:
         import torch
         if out is None:
             rows, dev = self.read_rows(), self.device
-            k = torch.empty((rows, self.Hkv, self.d), dtype=torch.float16 if dtype is None else dtype, device=dev)
-            v = torch.empty_like(k)
-            pos = torch.empty(rows, dtype=torch.int32, device=dev)
-            cu = torch.empty(self.B + 1, dtype=torch.int32, device=dev)
+            with allocating_on(stream):
+                k = torch.empty((rows, self.Hkv, self.d), dtype=torch.float16 if dtype is None else dtype, device=dev)
+                v = torch.empty_like(k)
+                pos = torch.empty(rows, dtype=torch.int32, device=dev)
+                cu = torch.empty(self.B + 1, dtype=torch.int32, device=dev)
             out = {"k": k, "v": v, "positions": pos, "cu_seqlens": cu}
             k_at, v_at, ks = k.data_ptr(), v.data_ptr(), _PAIR.pack(self.Hkv * self.d, self.d)
             vs = ks

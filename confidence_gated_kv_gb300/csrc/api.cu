@@ -421,7 +421,10 @@ int confkv_read_layer(confkv_ctx* ctx, int32_t layer, int32_t dtype, void* k, vo
     if (!k_stride || !v_stride || !positions || !aligned(positions, 4)) return CONFKV_EINVAL;
     if (!packed_rows_ok(k, k_stride, s, rows) || !packed_rows_ok(v, v_stride, s, rows)) return CONFKV_EINVAL;
   }
-  const long long n8 = std::min<long long>(s.cap, ctx->n8_bound + ctx->pin_left);
+  // a captured read may be replayed after any number of steps
+  const long long n8 = refuse_capture(as_stream(stream)) == CONFKV_OK
+                           ? std::min<long long>(s.cap, ctx->n8_bound + ctx->pin_left)
+                           : s.cap;
   return launch_read_layer(s, ctx->d, layer, dtype == CONFKV_BF16, k, v, rows > 0 ? k_stride : none,
                            rows > 0 ? v_stride : none, positions, cu, (int)rows, n8, as_stream(stream)) == 0
              ? CONFKV_OK

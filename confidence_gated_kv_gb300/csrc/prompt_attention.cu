@@ -68,7 +68,6 @@ struct Args {
   float* lse;
   float scale, scale2;                   // scale2 = scale * log2(e)
   int wide;                              // rows of out start on 32-byte boundaries
-  int32_t* status;
 };
 
 struct Item {                            // what one CTA computes
@@ -133,9 +132,11 @@ __device__ bool find_item(const Args& a, int tile, int head, int rank, int split
   return false;
 }
 
+__device__ int32_t g_prompt_status;      // one word per device: a bounded wait gave up
+
 // Bounded wait (about four seconds); false once it, or another wait of the
 // CTA, has given up.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (bar_try(bar, parity)) return true;
   const long long start = clock64();
   do {
@@ -143,7 +144,7 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
     if (*abort) return false;
   } while (clock64() - start < (1LL << 33));
   *abort = 1;
-  atomicOr(status, kStatusTimeout);
+  atomicOr(&g_prompt_status, kStatusTimeout);
   return false;
 }
 
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = s_tmem;
 
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_on(bar, parity, &s_abort, a.status); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_on(bar, parity, &s_abort); };
   auto all = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(bar, parity)); };
   // Item k of this CTA, by a whole warp; false at the end of the work.
   auto get_item = [&](int k, Item& it) {
@@ -707,23 +708,7 @@ bool encode(CUtensorMap* m, const void* p, bool bf16, int d, long long heads, lo
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-__device__ int32_t g_prompt_status;      // one word per device: a bounded wait gave up
-
 std::mutex g_mu;
-int32_t* g_status_addr[kMaxDevices] = {};
-
-int status_word(int32_t** out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return CONFKV_ECUDA;
-  std::lock_guard<std::mutex> lock(g_mu);
-  if (!g_status_addr[dev]) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_prompt_status) != cudaSuccess) return CONFKV_ECUDA;
-    g_status_addr[dev] = static_cast<int32_t*>(p);
-  }
-  *out = g_status_addr[dev];
-  return CONFKV_OK;
-}
 
 template <int D, bool BF16, bool SPLIT>
 int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, long long items,
@@ -809,7 +794,7 @@ using namespace confkv;
 extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream) {
   if (!p) return CONFKV_EINVAL;
   if (p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->total_q < 0 || p->total_k < 0) return CONFKV_EINVAL;
-  if (p->Hq % p->Hkv || p->Hq / p->Hkv > kRows) return CONFKV_EINVAL;
+  if (p->Hq % p->Hkv || p->Hq / p->Hkv > kRows || p->reserved != 0) return CONFKV_EINVAL;
   if (p->dtype != CONFKV_Q_FP16 && p->dtype != CONFKV_Q_BF16) return CONFKV_EINVAL;
   if (p->d != 64 && p->d != 128) return CONFKV_ENOTIMPL;
   if (!std::isfinite(p->scale) || !(p->scale > 0.f)) return CONFKV_EINVAL;
@@ -851,8 +836,6 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
       !encode(&mv, keys ? p->v : p->q, bf16, p->d, keys ? p->Hkv : 1, keys ? p->total_k : 1, p->v_stride[0],
               p->v_stride[1], 1, kKeys))
     return CONFKV_EINVAL;
-  const int r = status_word(&a.status);
-  if (r != CONFKV_OK) return r;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Plan plan = plan_items(tiles * p->Hkv, (double)p->total_k / p->B / kKeys);
   auto fn = p->d == 128 ? (bf16 ? launch<128, true> : launch<128, false>)
@@ -867,9 +850,8 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
 
 extern "C" int confkv_prompt_status(int32_t* bits, void* stream) {
   if (!bits) return CONFKV_EINVAL;
-  int32_t* word = nullptr;
-  const int r = status_word(&word);
-  if (r != CONFKV_OK) return r;
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, g_prompt_status) != cudaSuccess) return CONFKV_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int32_t host = 0;
   cudaError_t e = cudaMemcpyAsync(&host, word, 4, cudaMemcpyDeviceToHost, st);

@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from .binding import FP32, _check, _stream, dtype_code, lib, on_device
+from .binding import FP32, _check, _stream, allocating_on, dtype_code, lib, on_device
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -82,9 +82,22 @@ def _vector(t, name, n, dtype, dev):
     return t.data_ptr()
 
 
-def _like(t):
-    """New contiguous tensor of the shape, type and device of t."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _like(t, stream):
+    """New contiguous tensor of the shape, type and device of t, to be written
+    on `stream`."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    with allocating_on(stream):
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _no_gradients(*tensors):
+    """The operators have no backward pass: a result that autograd would treat
+    as a constant is refused rather than returned."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                _unfit("an input requires gradients, which this operator does not give: call it under torch.no_grad()")
 
 
 def _launch(fn, name, args, dev, stream):
@@ -100,13 +113,15 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
     q [n, Hq, d] and k [n, Hkv, d] at int32 `positions` [n].  `rotary` may be
     None (norms only), k None (queries only).  Returns (q_out, k_out): new
     tensors of the inputs' type, or the given ones, which may be of another
-    type, strided, or the inputs themselves."""
+    type, strided, or the inputs themselves.  No backward pass: inputs that
+    require gradients are refused while gradients are enabled."""
     if torch is None:
         _bind()
     (n, Hq, d), qs = _dims(q, "q")
+    _no_gradients(q, k, q_weight, k_weight)
     dev, code = q.get_device(), dtype_code(q.dtype)
     if q_out is None:
-        q_out, qo_code, qos = _like(q), code, (Hq * d, d)
+        q_out, qo_code, qos = _like(q, stream), code, (Hq * d, d)
     else:
         shape, qos = _dims(q_out, "q_out", dev)
         qo_code = dtype_code(q_out.dtype)
@@ -120,7 +135,7 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
         if nk != n or dk != d or k.dtype != q.dtype:
             _unfit("k: rows, channels and type of q are wanted")
         if k_out is None:
-            k_out, ko_code, kos = _like(k), code, (Hkv * d, d)
+            k_out, ko_code, kos = _like(k, stream), code, (Hkv * d, d)
         else:
             shape, kos = _dims(k_out, "k_out", dev)
             ko_code = dtype_code(k_out.dtype)
@@ -153,10 +168,14 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     device): first query row of each sequence and the end; cu_seqlens_k the
     same for keys (default: cu_seqlens).  With `causal` the queries are the
     last of their sequence's keys.  scale defaults to 1 / sqrt(d).  Returns
-    out, or (out, lse) with return_lse; lse is fp32 [rows, Hq]."""
+    out, or (out, lse) with return_lse; lse is fp32 [rows, Hq].  No backward
+    pass: inputs that require gradients are refused while gradients are
+    enabled.  A sequence's last bits may depend on the sizes of the whole call:
+    the keys of few rows are split over more of the GPU and joined."""
     if torch is None:
         _bind()
     (nq, Hq, d), qs = _dims(q, "q")
+    _no_gradients(q, k, v)
     dev, dtype = q.get_device(), q.dtype
     (nk, Hkv, dk), ks = _dims(k, "k", dev)
     shape, vs = _dims(v, "v", dev)
@@ -167,7 +186,7 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     if cu_seqlens_k is not None:
         cuk_at = _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, torch.int32, dev)
     if out is None:
-        out, os = _like(q), (Hq * d, d)
+        out, os = _like(q, stream), (Hq * d, d)
     else:
         shape, os = _dims(out, "out", dev)
         if shape != q.shape or out.dtype != dtype:
@@ -178,7 +197,8 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
             _unfit("lse: a contiguous fp32 [rows, heads] tensor on the device of q is wanted")
         lse_at = lse.data_ptr()
     elif return_lse:
-        lse = torch.empty((nq, Hq), dtype=torch.float32, device=q.device)
+        with allocating_on(stream):
+            lse = torch.empty((nq, Hq), dtype=torch.float32, device=q.device)
         lse_at = lse.data_ptr()
     args = _PROMPT.pack(B, Hq, Hkv, d, dtype_code(dtype), 1 if causal else 0, nq, nk,
                         d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),

@@ -264,3 +264,76 @@ def test_many_sequences():
     o = a.read_layer(0)
     assert o["cu_seqlens"].tolist() == [sum(lens[:i]) for i in range(701)]
     assert o["positions"].tolist() == [p for n in lens for p in range(n)]
+
+
+def test_captured_read_follows_a_growing_cache():
+    # captured when the INT8 region is empty, replayed when it is not
+    w = Workload(name="grow", B=2, L=1, Hq=4, Hkv=2, d=64, V=1000, T0=10, steps=60, n_high=(200,), n_low=(200,), P=4,
+                 W=16, q_dtype="f16")
+    lens = [10, 4]
+    ks, vs = packed(lens, 1, 2, 64, F16, 9)
+    cache = ck.Cache(ck.config_from_workload(w, cap=256))
+    by_layer(cache, ks, vs, lens)
+    out = dict(k=torch.empty((200, 2, 64), dtype=F16, device="cuda"), positions=torch.empty(200, dtype=torch.int32, device="cuda"),
+               cu_seqlens=torch.empty(3, dtype=torch.int32, device="cuda"))
+    out["v"] = torch.empty_like(out["k"])
+    cache.read_layer(0, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        cache.read_layer(0, out=out)
+    for i in range(50):
+        cache.step(*(x.cuda() for x in step_inputs(w, 3, i)))
+    graph.replay()
+    want = cache.read_layer(0)
+    n = int(want["cu_seqlens"][2])
+    assert n == 10 + 4 + 2 * 50
+    assert torch.equal(out["cu_seqlens"], want["cu_seqlens"])
+    for key in ("k", "v", "positions"):
+        assert torch.equal(out[key][:n], want[key][:n])
+
+
+def test_read_on_another_stream():
+    lens = [300, 50]
+    ks, vs = packed(lens, 1, 2, 128, F16, 10)
+    cache = ck.Cache(config(lens, 1))
+    by_layer(cache, ks, vs, lens)
+    want = cache.read_layer(0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        got = cache.read_layer(0, stream=s)
+    s.synchronize()
+    for key in want:
+        assert torch.equal(got[key], want[key])
+
+
+def test_refusals_on_the_device():
+    lens = [40]
+    ks, vs = packed(lens, 1, 2, 128, F16, 11)
+    cache = ck.Cache(config(lens, 1))
+    with pytest.raises(ValueError):
+        cache.prefill_begin([40, 1])
+    with pytest.raises(ck.ConfkvError):
+        cache.prefill_begin([-1])
+    cache.prefill_begin(lens)
+    k, v = ks[0], vs[0]
+    for a, b in ((k[:39], v[:39]), (k, v.to(BF16)), (k[:, :1], v[:, :1]), (k.cpu(), v.cpu()), (k[:, :, :64], v[:, :, :64]),
+                 (k.transpose(1, 2).contiguous().transpose(1, 2), v)):
+        with pytest.raises(ValueError):
+            cache.prefill_layer(0, a, b)
+    with pytest.raises(ck.ConfkvError):                                  # heads that overlap
+        cache.prefill_layer(0, k[:, :1].expand(-1, 2, -1), v)
+    with pytest.raises(ck.ConfkvError):
+        cache.prefill_layer(1, k, v)
+    with pytest.raises(ck.ConfkvError):
+        cache.prefill_layer(-1, k, v)
+    cache.prefill_layer(0, k, v)
+    o = cache.read_layer(0)
+    for bad in (dict(o, positions=o["positions"].long()), dict(o, cu_seqlens=o["cu_seqlens"][:1]), dict(o, v=o["v"].to(BF16)),
+                dict(o, k=o["k"][:39])):
+        with pytest.raises(ValueError):
+            cache.read_layer(0, out=bad)
+    with pytest.raises(ck.ConfkvError):
+        cache.read_layer(3)
+    with pytest.raises(ValueError):
+        cache.read_layer(0, dtype=torch.int32)

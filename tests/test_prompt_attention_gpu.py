@@ -11,6 +11,10 @@ Tolerance per output element, with u = eps / 2 of the type (bf16 2^-8, fp16
   - sums over n keys, the exponential (2^-22 each):               2 (n + 4) 2^-22 A
 """
 import math
+import os
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -209,3 +213,90 @@ def test_same_result_every_time_on_streams_and_in_graphs():
     q.copy_(q2), k.copy_(k2), v.copy_(v2), c.copy_(torch.tensor([0, 800, 814, 814], dtype=torch.int32))
     graph.replay()
     assert torch.equal(out, want2)
+
+
+def test_split_keys_agree_with_whole_ones():
+    # few rows against long keys are split over CTAs and warpgroups, many rows
+    # are not: both within the tolerance of the same reference
+    for lq, lk in (([2], [3000]), ([26], [1500]), ([51], [700]), ([1] * 12, [1 + 300 * i for i in range(12)])):
+        check(*inputs(lq, lk, 40, 8, 128, BF16, 21), lq, lk)
+        check(*inputs(lq, lk, 6, 2, 64, F16, 22), lq, lk)
+
+
+def test_first_call_of_a_process_may_be_captured():
+    code = (
+        "import torch, confidence_gated_kv_gb300 as ck\n"
+        "q = torch.randn(70, 4, 64, device='cuda').half()\n"
+        "c = torch.tensor([0, 70], dtype=torch.int32, device='cuda')\n"
+        "p = torch.arange(70, dtype=torch.int32, device='cuda')\n"
+        "r, out, o2 = ck.Rotary(64), torch.zeros_like(q), torch.zeros_like(q)\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    ck.prompt_attention(q, q, q, c, out=out)\n"
+        "    ck.qk_rotary(q, None, p, r, q_out=o2)\n"
+        "g.replay()\n"
+        "torch.cuda.synchronize()\n"
+        "assert torch.equal(out, ck.prompt_attention(q, q, q, c))\n"
+        "assert torch.equal(o2, ck.qk_rotary(q, None, p, r)[0])\n"
+        "assert ck.prompt_status() == 0\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_calls_from_two_threads():
+    lens = [400, 33]
+    data = [inputs(lens, lens, 10, 2, 128, BF16, s) for s in (31, 32)]
+    c = cu(lens)
+    want = [ck.prompt_attention(*x, c) for x in data]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(50):
+            got[i] = ck.prompt_attention(*data[i], c, stream=s)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_inputs_that_require_gradients_are_refused():
+    q, k, v = inputs([9], [9], 2, 1, 64, F16, 23)
+    for x in (q, k, v):
+        x.requires_grad_(True)
+        with pytest.raises(ValueError):
+            ck.prompt_attention(q, k, v, cu([9]))
+        with torch.no_grad():
+            ck.prompt_attention(q, k, v, cu([9]))
+        x.requires_grad_(False)
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError):
+        ck.qk_rotary(q, k, None, None, w)
+
+
+def test_refusals_on_the_device():
+    q, k, v = inputs([20], [20], 4, 2, 64, F16, 24)
+    c = cu([20])
+    with pytest.raises(ck.ConfkvError):                                 # broadcast heads
+        ck.prompt_attention(q, k[:, :1].expand(-1, 2, -1), v, c)
+    with pytest.raises(ck.ConfkvError):                                 # rows off a 16-byte boundary
+        ck.prompt_attention(torch.zeros(20, 4, 65, device="cuda", dtype=F16)[:, :, 1:], k, v, c)
+    for bad in (dict(scale=0.0), dict(scale=float("nan"))):
+        with pytest.raises(ck.ConfkvError):
+            ck.prompt_attention(q, k, v, c, **bad)
+    with pytest.raises(ck.ConfkvError):
+        ck.prompt_attention(q.float(), k.float(), v.float(), c)
+    for args in ((q, k[:19], v, c), (q, k, v.float(), c), (q, k, v, c.long()), (q, k, v, c.cpu()), (q, k.cpu(), v, c)):
+        with pytest.raises(ValueError):
+            ck.prompt_attention(*args)
+    with pytest.raises(ValueError):
+        ck.prompt_attention(q, k, v, c, out=torch.empty(20, 4, 64, device="cuda"))
+    with pytest.raises(ValueError):
+        ck.prompt_attention(q, k, v, c, lse=torch.empty(4, 20, device="cuda"))
+
