@@ -85,12 +85,22 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t top, uint32_t w) {
 
 // 8 values as words whose low byte is clamp(rint(x / s), -127, 127) + 128,
 // with the IEEE quotient.  x * (1 / s) is within 2 ulp of it (2^-15 up to
-// 127), so the integers agree unless the product lies that close to a half;
-// only then, or for a NaN, are the quotients computed.  Adding 1.5 2^23 + 128
-// rounds to an integer (ties to even) and leaves the stored byte in the low
-// bits.  No clamp: |x| <= 127 s (1 + 2^-23).
-__device__ __noinline__ uint32_t exact_code(float x, float s) {
-  return (uint32_t)((int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f) + kCodeBias);
+// 127), so the integers agree unless the product lies that close to a half.
+// Adding 1.5 2^23 + 128 rounds to an integer (ties to even) and leaves the
+// stored byte in the low bits.  No clamp: |x| <= 127 s (1 + 2^-23).
+//
+// Next to the half-integer h: the sign of e = x - h s, which one fused
+// multiply-add gives (and exactly where e is small: h s has at most 32 bits),
+// says on which side the quotient lies, and |e| <= s ulp(h) / 2 that it
+// rounds to h itself, a tie (to even).  Below 1/2 the spacing is half as
+// wide.  No quotient of two floats lies midway between two others.
+__device__ __noinline__ uint32_t code_next_to_half(float x, float s, float n, float off) {
+  const float h = n + copysignf(0.5f, off);
+  const float e = fmaf(-h, s, x);
+  float step = __uint_as_float((__float_as_uint(h) & 0x7f800000u) - (24u << 23));
+  if (fabsf(h) == 0.5f && (e < 0.f) == (h > 0.f)) step *= 0.5f;
+  const float c = fabsf(e) <= s * step ? rintf(h) : e > 0.f ? h + 0.5f : h - 0.5f;
+  return (uint32_t)((int)fminf(fmaxf(c, -127.f), 127.f) + kCodeBias);     // a NaN becomes -127
 }
 template <bool BF16>
 __device__ __forceinline__ void quantise8(const uint4& raw, const float (&scale)[8], const float (&inv)[8],
@@ -115,10 +125,12 @@ __device__ __forceinline__ void quantise8(const uint4& raw, const float (&scale)
     r[j] = __float_as_uint(whole.get().x);
     r[j + 1] = __float_as_uint(whole.get().y);
   }
-  if (near) {                                          // only the values that are near: a tie is not rare for
-#pragma unroll                                         // a channel whose absmax is a power of two
-    for (int j = 0; j < 8; ++j)
-      if (!(fabsf(q[j] - (__uint_as_float(r[j]) - kRound)) <= 0.49993f)) r[j] = exact_code(x[j], scale[j]);
+  if (near) {                                          // not rare for a channel whose absmax has few bits
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float n = __uint_as_float(r[j]) - kRound, off = q[j] - n;
+      if (!(fabsf(off) <= 0.49993f)) r[j] = code_next_to_half(x[j], scale[j], n, off);
+    }
   }
 }
 
@@ -212,24 +224,29 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
         const int p = i * 16 + token(quad * 4 + j);
         x[j] = p < n8 ? row(p) : make_uint4(0, 0, 0, 0);
       }
-      uint32_t r[4][8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) quantise8<BF16>(x[j], scale, inv, r[j]);
       if (IS_V) {
+        uint32_t word[8], r[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          quantise8<BF16>(x[j], scale, inv, r);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)                  // byte j of each channel's word
+            word[c] = j == 0 ? r[c] : __byte_perm(word[c], r[c], j == 1 ? 0x3240 : j == 2 ? 0x3410 : 0x4210);
+        }
         uint8_t* o = blk + (ch >> 2) * kChunk + (ch & 3) * 4 + (lane / kPer + kRowsPerWarp * quad) * 16;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint32_t*>(o + c * 64) = __byte_perm(__byte_perm(r[0][c], r[1][c], 0x0040),
-                                                                 __byte_perm(r[2][c], r[3][c], 0x0040), 0x5410);
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint32_t*>(o + c * 64) = word[c];
       } else {                                         // k8_offset
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          uint32_t r[8];
+          quantise8<BF16>(x[j], scale, inv, r);
           const int tau = token(quad * 4 + j);
           uint8_t* o = blk + ((ch >> 3) + (tau >> 3) * (D / 64)) * kChunk + ((ch >> 1) & 3) * 4 + (ch & 1) * 2 +
                        (tau & 7) * 64;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint16_t*>(o + c * 16) = (uint16_t)__byte_perm(r[j][2 * c], r[j][2 * c + 1], 0x0040);
+            *reinterpret_cast<uint16_t*>(o + c * 16) = (uint16_t)__byte_perm(r[2 * c], r[2 * c + 1], 0x0040);
         }
       }
     }
@@ -280,7 +297,7 @@ __device__ __forceinline__ void write_unit(const Shape& s, const Dev& d, int lay
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kWriteWarps * 32, 4)
+__global__ void __launch_bounds__(kWriteWarps * 32, 3)
     write_layer_kernel(Shape s, Dev d, int layer, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                        long long k_t, long long k_h, long long v_t, long long v_h) {
   extern __shared__ __align__(16) uint8_t smem[];      // an interleaved block per warp
