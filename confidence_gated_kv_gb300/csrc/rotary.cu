@@ -117,7 +117,7 @@ __device__ __forceinline__ void angle(const RotArgs& a, int pos, int i, float* c
 // threads take a row each, two 8-channel chunks per thread, with the next
 // row in flight.  (One thread computing its own angles for four heads, without
 // shared memory, was bound by instructions: 49 us for 8192 tokens of 48
-// heads of 128 channels against 38 now.)
+// heads of 128 channels against 36 now.)
 constexpr int kMaxTokens = 16;
 template <int TPR, int IN>
 __global__ void __launch_bounds__(256, 4) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
@@ -317,10 +317,10 @@ template <int TPR>
 void launch_rows(RotArgs a, cudaStream_t st) {
   constexpr int groups = 256 / TPR;
   const int heads = a.Hq + a.Hkv;
-  // Blocks of at least four rows per thread group, whole tokens; with few
+  // Blocks of about six rows per thread group, whole tokens; with few
   // tokens, fewer rows and then parts of the heads, until the blocks cover the
   // GPU twice or a thread group has one row left.
-  const int most = std::min(kMaxTokens, std::max(1, 4 * groups / heads));
+  const int most = std::min(kMaxTokens, std::max(1, 6 * groups / heads));
   a.tokens = (int)std::max<long long>(1, std::min<long long>(most, a.n / 304));
   const long long blocks = ((long long)a.n + a.tokens - 1) / a.tokens;
   const int parts = (int)std::max<long long>(1, std::min<long long>((heads + groups - 1) / groups, 304 / blocks));
