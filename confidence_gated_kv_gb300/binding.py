@@ -181,15 +181,22 @@ _same = contextlib.nullcontext()
 _current_device = None
 
 
-def on_device(index: int):
-    """Context in which device `index` is the current one (launches go to the
-    current device); nothing to do when it already is."""
+def call_on(index: int, fn, name: str, args: tuple, stream):
+    """fn(*args, stream) with device `index` current (launches go to the
+    current device) on `stream`, or the device's current stream when None."""
     global _current_device
-    import torch
     if _current_device is None:
+        import torch
         torch.cuda.init()
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    return _same if index == _current_device() else torch.cuda.device(index)
+    if index == _current_device():
+        status = fn(*args, _stream(stream, index))
+    else:
+        import torch
+        with torch.cuda.device(index):
+            status = fn(*args, _stream(stream, index))
+    if status:
+        _check(status, name)
 
 
 def allocating_on(stream):
@@ -281,6 +288,7 @@ class Cache:
         self._fn_step = lib().confkv_step
         self._dev_index = self.device.index if self.device.index is not None else torch.cuda.current_device()
         self.L, self.B, self.Hq, self.Hkv, self.d, self.V = cfg.L, cfg.B, cfg.Hq, cfg.Hkv, cfg.d, cfg.V
+        self._packed_strides = _PAIR.pack(cfg.Hkv * cfg.d, cfg.d)
         self.cap = (cfg.cap + 15) // 16 * 16
         self.WR = (cfg.W + 16 + 15) // 16 * 16
         self.max_evict = cfg.max_evict if cfg.max_evict > 0 else self.cap + self.WR
@@ -314,9 +322,8 @@ class Cache:
         ints).  Write every layer with prefill_layer, then step."""
         if len(prefill_len) != self.B:
             raise ValueError("prefill_len: one length per sequence is wanted")
-        with on_device(self._dev_index):
-            _check(lib().confkv_prefill_begin(self._h, struct.pack("=%di" % self.B, *prefill_len),
-                                              _stream(stream, self._dev_index)), "confkv_prefill_begin")
+        call_on(self._dev_index, lib().confkv_prefill_begin, "confkv_prefill_begin",
+                (self._h, struct.pack("=%di" % self.B, *prefill_len)), stream)
         self._prompt_rows = sum(prefill_len)
 
     def _packed(self, t, name, rows):
@@ -339,11 +346,8 @@ class Cache:
         v_at, vs = self._packed(v, "v", rows)
         if k.dtype != v.dtype:
             raise ValueError("k and v: one type is wanted")
-        with on_device(self._dev_index):
-            st = lib().confkv_prefill_layer(self._h, layer, k_at, v_at, dtype_code(k.dtype), ks, vs,
-                                            _stream(stream, self._dev_index))
-        if st:
-            _check(st, "confkv_prefill_layer")
+        call_on(self._dev_index, lib().confkv_prefill_layer, "confkv_prefill_layer",
+                (self._h, layer, k_at, v_at, dtype_code(k.dtype), ks, vs), stream)
 
     def read_rows(self) -> int:
         """Rows that always hold a layer's resident entries (exact until the
@@ -359,15 +363,15 @@ class Cache:
         and type.  Sequence b has rows cu_seqlens[b] to cu_seqlens[b + 1]."""
         import torch
         if out is None:
-            rows, dev = self.read_rows(), self.device
-            with allocating_on(stream):
-                k = torch.empty((rows, self.Hkv, self.d), dtype=torch.float16 if dtype is None else dtype, device=dev)
+            rows, dev, empty = self.read_rows(), self.device, torch.empty
+            with _same if stream is None else allocating_on(stream):
+                k = empty((rows, self.Hkv, self.d), dtype=torch.float16 if dtype is None else dtype, device=dev)
                 v = torch.empty_like(k)
-                pos = torch.empty(rows, dtype=torch.int32, device=dev)
-                cu = torch.empty(self.B + 1, dtype=torch.int32, device=dev)
+                pos = empty(rows, dtype=torch.int32, device=dev)
+                cu = empty(self.B + 1, dtype=torch.int32, device=dev)
             out = {"k": k, "v": v, "positions": pos, "cu_seqlens": cu}
-            k_at, v_at, ks = k.data_ptr(), v.data_ptr(), _PAIR.pack(self.Hkv * self.d, self.d)
-            vs = ks
+            k_at, v_at = k.data_ptr(), v.data_ptr()
+            ks = vs = self._packed_strides
         else:
             k, v, pos, cu = out["k"], out["v"], out["positions"], out["cu_seqlens"]
             rows = k.shape[0]
@@ -378,11 +382,8 @@ class Cache:
             for name, t, n in (("positions", pos, rows), ("cu_seqlens", cu, self.B + 1)):
                 if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != k.device:
                     raise ValueError("%s: a contiguous int32 vector of %d on the cache's device is wanted" % (name, n))
-        with on_device(self._dev_index):
-            st = lib().confkv_read_layer(self._h, layer, dtype_code(k.dtype), k_at, v_at, ks, vs, pos.data_ptr(),
-                                         cu.data_ptr(), rows, _stream(stream, self._dev_index))
-        if st:
-            _check(st, "confkv_read_layer")
+        call_on(self._dev_index, lib().confkv_read_layer, "confkv_read_layer",
+                (self._h, layer, dtype_code(k.dtype), k_at, v_at, ks, vs, pos.data_ptr(), cu.data_ptr(), rows), stream)
         return out
 
     def new_outputs(self):

@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from .binding import FP32, _check, _stream, allocating_on, dtype_code, lib, on_device
+from .binding import FP32, _check, _stream, allocating_on, call_on, dtype_code, lib
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -100,13 +100,6 @@ def _no_gradients(*tensors):
                 _unfit("an input requires gradients, which this operator does not give: call it under torch.no_grad()")
 
 
-def _launch(fn, name, args, dev, stream):
-    with on_device(dev):
-        st = fn(args, _stream(stream, dev))
-    if st:
-        _check(st, name)
-
-
 def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
               stream=None):
     """Per-head RMS norm (where a weight is given) and rotary rotation of
@@ -157,7 +150,7 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
     args = _ROTARY.pack(n, Hq, Hkv, d, rot, interleaved, code, w_code, qo_code, ko_code, eps, mscale, q.data_ptr(),
                         k_at, q_out.data_ptr(), ko_at, qs[0], qs[1], ks[0], ks[1], qos[0], qos[1], kos[0], kos[1],
                         qw_at, kw_at, pos_at, turns_at)
-    _launch(lib().confkv_qk_rotary, "confkv_qk_rotary", args, dev, stream)
+    call_on(dev, lib().confkv_qk_rotary, "confkv_qk_rotary", (args,), stream)
     return q_out, k_out
 
 
@@ -203,7 +196,7 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     args = _PROMPT.pack(B, Hq, Hkv, d, dtype_code(dtype), 1 if causal else 0, nq, nk,
                         d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                         out.data_ptr(), lse_at, cu_at, cuk_at, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1])
-    _launch(lib().confkv_prompt_attention, "confkv_prompt_attention", args, dev, stream)
+    call_on(dev, lib().confkv_prompt_attention, "confkv_prompt_attention", (args,), stream)
     return (out, lse) if return_lse else out
 
 
