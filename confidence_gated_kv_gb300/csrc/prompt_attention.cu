@@ -544,6 +544,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tiles += nw;
       if (!ok) break;
+      // What the last product does not bear on goes before its wait.
+      uint16_t* dst = nullptr;
+      float inv = 0.f;                                  // rows without a key are zero
+      if (!SPLIT && valid) {
+        const long long at = it.q0 + t;
+        const int head = it.head * a.G + row % a.G;
+        dst = a.out + at * a.out_token + head * a.out_head;
+        inv = seen > 0 ? 1.f / l : 0.f;
+        if (a.lse)
+          a.lse[at * a.Hq + head] = seen > 0 ? (ref == -INFINITY ? 0.f : ref * a.scale) + logf(l) : -INFINITY;
+      }
       if (nw > 0) {
         ok = all(o_full(w), items & 1);
         if (!ok) break;
@@ -554,9 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         in_item = true;
         continue;                                       // merged below
       }
-      // Rows without a key are zero.
-      const float inv = seen > 0 ? 1.f / l : 0.f;
-      uint16_t* dst = a.out + (long long)(it.q0 + t) * a.out_token + (long long)(it.head * a.G + row % a.G) * a.out_head;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -580,9 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       fence_before();                                   // the next product overwrites the accumulator
-      if (a.lse && valid)
-        a.lse[(long long)(it.q0 + t) * a.Hq + it.head * a.G + row % a.G] =
-            seen > 0 ? (ref == -INFINITY ? 0.f : ref * a.scale) + logf(l) : -INFINITY;
+      __syncwarp();
     }
     __syncwarp();
     regs_dec<kRegs>();
