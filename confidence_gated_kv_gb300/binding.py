@@ -312,10 +312,10 @@ class Cache:
     def prefill(self, k, v, prefill_len: Sequence[int], stream=None):
         """k, v: device fp16 [L][B][Hkv][t_max][d]."""
         t_max = int(k.shape[3])
-        self._prompt_rows = None
         pl = (ctypes.c_int32 * self.B)(*[int(x) for x in prefill_len])
         _check(lib().confkv_prefill(self._h, pl, _ptr(k), _ptr(v), t_max, _stream(stream)),
                "confkv_prefill")
+        self._prompt_rows = None
 
     def prefill_begin(self, prefill_len: Sequence[int], stream=None):
         """Start a prefill by layer: prompt length of every sequence (host

@@ -19,8 +19,8 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <climits>
 #include <cmath>
-#include <cstring>
 #include <mutex>
 #include <type_traits>
 
@@ -84,35 +84,52 @@ __device__ __forceinline__ int key_tiles(const Item& it) { return it.dual ? it.n
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
-// Sequence and tile of work item `tile`, by one warp.  Lengths are clamped to
-// the packed tensors, so no array content leads out of them.
-// CTA `rank` of `split` takes its share of the item's key tiles.
-__device__ bool find_item(const Args& a, int tile, int head, int rank, int split, Item* it) {
+// Where a search for an item got to: the first sequence of a group and the
+// tiles before it.  A CTA's items mostly follow each other.
+struct Search {
+  int b0 = 0, before = 0;
+};
+
+// Sequence and tile of work item `tile`, by one warp, W sequences per lane at
+// a time (one where that is enough: the CTA's next item waits for this; with
+// four for every batch the eight ragged prompts took 104 us instead of 99).
+// Lengths are clamped to the packed tensors, so no array content
+// leads out of them.  CTA `rank` of `split` takes its share of the item's key
+// tiles.
+template <int W>
+__device__ __forceinline__ bool find_in_groups(const Args& a, int tile, int head, int rank, int split, Search& at, Item* it) {
   const int lane = threadIdx.x & 31;
   const int per = 2 * a.tokens;
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int q0 = 0, lq = 0, k0 = 0, lk = 0;
-    if (b < a.B) {
-      const int qa = a.cu_q[b], qb = a.cu_q[b + 1], ka = a.cu_k[b], kb = a.cu_k[b + 1];
-      q0 = clampi(qa, 0, a.total_q);
-      lq = clampi(qb, q0, a.total_q) - q0;
-      k0 = clampi(ka, 0, a.total_k);
-      lk = clampi(kb, k0, a.total_k) - k0;
+  if (tile < at.before) at = Search{};
+  for (; at.b0 < a.B; at.b0 += 32 * W) {
+    const int b = at.b0 + lane * W;
+    int q[W + 1], k[W + 1], tiles[W], own = 0;
+#pragma unroll
+    for (int i = 0; i <= W; ++i) {
+      q[i] = a.cu_q[min(b + i, a.B)];
+      k[i] = a.cu_k[min(b + i, a.B)];
     }
-    const int nt = (lq + per - 1) / per;
-    int sum = nt;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int q0 = clampi(q[i], 0, a.total_q);
+      tiles[i] = b + i < a.B ? (clampi(q[i + 1], q0, a.total_q) - q0 + per - 1) / per : 0;
+      own += tiles[i];
+    }
+    int sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += x;
     }
-    const bool mine = tile >= before + sum - nt && tile < before + sum;
-    const unsigned hit = __ballot_sync(0xffffffffu, mine);
-    if (hit) {
-      if (mine) {
-        const int t0 = (nt - 1 - (tile - (before + sum - nt))) * per;   // the longest rows first
+    int start = at.before + sum - own;
+    bool mine = false;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (tile >= start && tile < start + tiles[i]) {
+        mine = true;
+        const int q0 = clampi(q[i], 0, a.total_q), lq = clampi(q[i + 1], q0, a.total_q) - q0;
+        const int k0 = clampi(k[i], 0, a.total_k), lk = clampi(k[i + 1], k0, a.total_k) - k0;
+        const int t0 = (tiles[i] - 1 - (tile - start)) * per;     // the longest rows first
         it->q0 = q0; it->lq = lq; it->k0 = k0; it->lk = lk;
         it->t0 = t0; it->head = head;
         const int mid = min(t0 + a.tokens, lq), end = min(t0 + per, lq);
@@ -125,11 +142,17 @@ __device__ bool find_item(const Args& a, int tile, int head, int rank, int split
         it->n0 = it->dual ? (to - from + 1) / 2 : clampi(n0 - from, 0, to - from);
         it->n1 = it->dual ? (to - from) / 2 : clampi(n1 - from, 0, to - from);
       }
-      return true;
+      start += tiles[i];
     }
-    before += __shfl_sync(0xffffffffu, sum, 31);
+    if (__any_sync(0xffffffffu, mine)) return true;
+    at.before += __shfl_sync(0xffffffffu, sum, 31);
   }
   return false;
+}
+
+__device__ __forceinline__ bool find_item(const Args& a, int tile, int head, int rank, int split, Search& at, Item* it) {
+  return a.B <= 32 ? find_in_groups<1>(a, tile, head, rank, split, at, it)
+                   : find_in_groups<4>(a, tile, head, rank, split, at, it);
 }
 
 __device__ int32_t g_prompt_status;      // one word per device: a bounded wait gave up
@@ -212,9 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this point touches memory that the previous kernel may write
   pdl_wait();
   const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0;
+  Search search;
   if (warp == 10) {
     const int index = a.item0 + blockIdx.x / split;     // an item per CTA, or per cluster
-    const bool found = find_item(a, index / a.Hkv, index % a.Hkv, rank, split, &s_item[0]);
+    const bool found = find_item(a, index / a.Hkv, index % a.Hkv, rank, split, search, &s_item[0]);
     if (lane == 0) s_item[0].found = found;
   }
   fence_before();
@@ -397,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k >= 2 && !all(item_empty(k), ((k >> 1) - 1) & 1)) return false;
         index += a.item0;
         const bool found =
-            index >= a.item0 && find_item(a, index / a.Hkv, index % a.Hkv, rank, split, &s_item[k & 1]);
+            index >= a.item0 && find_item(a, index / a.Hkv, index % a.Hkv, rank, split, search, &s_item[k & 1]);
         __syncwarp();
         if (lane == 0) {
           s_item[k & 1].found = found;
@@ -792,6 +816,12 @@ bool rows_ok(const void* p, const int64_t* stride, int d, long long tokens, long
   return true;
 }
 
+// No two rows share an element.
+bool rows_apart(const int64_t* stride, int d, long long tokens, long long heads) {
+  return tokens < 2 || heads < 2 || stride[0] >= (heads - 1) * stride[1] + d ||
+         stride[1] >= (tokens - 1) * stride[0] + d;
+}
+
 }  // namespace
 }  // namespace confkv
 
@@ -800,6 +830,8 @@ using namespace confkv;
 extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream) {
   if (!p) return CONFKV_EINVAL;
   if (p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->total_q < 0 || p->total_k < 0) return CONFKV_EINVAL;
+  constexpr int32_t most = INT32_MAX - 4096;             // a tile's end behind the last row fits 32 bits
+  if (p->total_q > most || p->total_k > most || p->B > most) return CONFKV_EINVAL;
   if (p->Hq % p->Hkv || p->Hq / p->Hkv > kRows || p->reserved != 0) return CONFKV_EINVAL;
   if (p->dtype != CONFKV_Q_FP16 && p->dtype != CONFKV_Q_BF16) return CONFKV_EINVAL;
   if (p->d != 64 && p->d != 128) return CONFKV_ENOTIMPL;
@@ -810,6 +842,7 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
   if (!p->q || !p->out || (p->total_k > 0 && (!p->k || !p->v))) return CONFKV_EINVAL;
   if (!rows_ok(p->q, p->q_stride, p->d, p->total_q, p->Hq) ||
       !rows_ok(p->out, p->out_stride, p->d, p->total_q, p->Hq) ||
+      !rows_apart(p->out_stride, p->d, p->total_q, p->Hq) ||
       !rows_ok(p->k, p->k_stride, p->d, p->total_k, p->Hkv) ||
       !rows_ok(p->v, p->v_stride, p->d, p->total_k, p->Hkv))
     return CONFKV_EINVAL;

@@ -525,14 +525,18 @@ int confkv_rotary_frequencies(int32_t rot, double base, int32_t scaling, double 
  *   lse: fp32 [total_q][Hq], or NULL.
  *   cu_q, cu_k: DEVICE int32 [B + 1], ascending from 0; values outside
  *   [0, total] are clamped to it.  Rows of out and lse that belong to no
- *   sequence are not written.
+ *   sequence are not written.  total_q, total_k < 2^31 - 4096.
  * Scores, maxima, sums and the accumulated output are fp32; the weights are
  * rounded to `dtype` for the product with v, the output once at the end.
  * Values of keys that no query of the call sees do not reach the output,
  * NaN and infinities among them; a non-finite value of v within a sequence
  * may reach rows up to 127 keys before it.  out must not overlap an input.
- * The call uses no workspace and may be captured.  Asynchronous on `stream`.
- * CONFKV_EINVAL for a bad argument, CONFKV_ENOTIMPL for another d.
+ * The keys of few rows are split over a cluster of CTAs and joined, by a rule
+ * on the sizes above: the same call gives the same bits every time, but a
+ * sequence's last bits may depend on the sizes of the call it is part of.
+ * The call uses no workspace and may be captured; two calls may run at once.
+ * Asynchronous on `stream`.  CONFKV_EINVAL for a bad argument,
+ * CONFKV_ENOTIMPL for another d.
  */
 typedef struct confkv_prompt_args {
   int32_t B, Hq, Hkv, d;

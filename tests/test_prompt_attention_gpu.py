@@ -123,6 +123,15 @@ def test_many_short_sequences():
     check(*inputs(lens, lens, 8, 2, 64, BF16, 5), lens, lens)
 
 
+def test_many_single_tokens():
+    # a decode step of many sequences: several groups of 128 offsets
+    g = torch.Generator().manual_seed(2)
+    lk = torch.randint(1, 200, (515,), generator=g).tolist()
+    check(*inputs([1] * 515, lk, 6, 2, 64, F16, 15), [1] * 515, lk)
+    lq = [min(n, i % 3) for i, n in enumerate(lk)]
+    check(*inputs(lq, lk, 4, 1, 64, BF16, 16), lq, lk)
+
+
 def test_long_history():
     check(*inputs([1], [33000], 5, 1, 128, BF16, 6), [1], [33000])
     check(*inputs([200, 1], [5000, 9001], 5, 1, 128, F16, 7), [200, 1], [5000, 9001])

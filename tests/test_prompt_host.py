@@ -23,11 +23,13 @@ def attention_args(**kw):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Hq=9), dict(Hq=258), dict(total_q=-1), dict(total_k=-1), dict(dtype=2),
+    dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Hq=9), dict(Hq=258), dict(total_q=-1), dict(total_k=-1), dict(total_q=2 ** 31 - 1),
+    dict(total_k=2 ** 31 - 100), dict(dtype=2),
     dict(dtype=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(q=0),
     dict(k=0), dict(v=0), dict(out=0), dict(cu_q=0), dict(cu_k=0), dict(cu_q=PTR + 2), dict(q=PTR + 8),
     dict(k=PTR + 2), dict(v=PTR + 4), dict(out=PTR + 8), dict(lse=PTR + 1), dict(qs=(1020, 128)),
-    dict(qs=(1024, 120)), dict(ks=(256, 0)), dict(vs=(-256, 128)), dict(os=(64, 128)),
+    dict(qs=(1024, 120)), dict(ks=(256, 0)), dict(vs=(-256, 128)), dict(os=(64, 128)), dict(os=(128, 128)),
+    dict(os=(512, 128)),
 ])
 def test_attention_refusals(bad):
     assert ck.lib().confkv_prompt_attention(attention_args(**bad), None) == binding.EINVAL
