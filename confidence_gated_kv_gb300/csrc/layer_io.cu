@@ -14,7 +14,10 @@
 // Read: the resident entries of a layer, dequantised, as packed rows: INT8
 // entries in slot order, then the FP16 window by position.
 //
-// Both move a few bytes per value and are bound by HBM.
+// Both move a few bytes per value.  Eight prompts of 4096 tokens, 8 KV heads,
+// d = 128: the write takes 73 us for 134 MB read and 71 MB written (30 of
+// them the absmax pass, at 4.4 TB/s; then the quantising instructions), the
+// read 40 us for 71 MB and 134 MB (5.1 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

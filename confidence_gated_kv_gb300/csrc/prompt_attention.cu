@@ -16,6 +16,14 @@
 // not started (the copies of the next item run behind the last tiles of the
 // current one); with few items the keys of an item are split over a cluster
 // of CTAs instead, which merge their parts through distributed shared memory.
+//
+// What bounds it: the chain of a tile, from its scores through the softmax
+// (about 1500 cycles, 700 of them the exponentials) and both products (1024)
+// to the next scores; two of them interleave and keep the tensor cores busy
+// for 70 % of the time.  Measured (bf16, 40 query heads on 8, d = 128): one
+// prompt of 16384 tokens 1.91 ms, 1.44 PFLOP/s; eight prompts of 1 to 2047
+// tokens 99 us; single tokens of eight sequences on 15 216 keys 25 us, with
+// K and V at 5 TB/s while they stream.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <algorithm>
