@@ -30,7 +30,6 @@
 #include <climits>
 #include <cmath>
 #include <mutex>
-#include <type_traits>
 
 #include "../../include/confkv.h"
 #include "confkv_internal.cuh"
@@ -661,20 +660,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (done) {
       const int per = a.tokens * a.G;                   // rows of a tile that are used
       const int rows = min(2 * a.tokens, it.lq - it.t0) * a.G;
-      constexpr int kVec = D / 32;                      // channels per lane
-      using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
-      for (int i = rank + split * warp; i < rows; i += split * (kThreads / 32)) {
+      constexpr int kLanes = D / 4;                     // per row: four channels each
+      const int col = (lane % kLanes) * 4, group = threadIdx.x / kLanes;
+      for (int i = rank + split * group; i < rows; i += split * (kThreads / kLanes)) {
         const int slot = i < per ? i : kRows + i - per, t = it.t0 + i / a.G;
         const int seen = a.causal ? clampi(it.lk - it.lq + t + 1, 0, it.lk) : it.lk;
         // the row's parts: one of each CTA, or with two warpgroups per row two
-        float top = -INFINITY, sum = 0.f, x[kVec] = {};
+        float top = -INFINITY, sum = 0.f, x[4] = {};
         for (int at = slot; at < (it.dual ? 2 * kRows : slot + 1); at += kRows) {
-          Vec y[kMaxSplit];
+          float4 y[kMaxSplit];
           float2 z[kMaxSplit];
 #pragma unroll
           for (int r = 0; r < kMaxSplit; ++r)           // all parts in flight
             if (r < split) {
-              y[r] = *reinterpret_cast<const Vec*>(cluster.map_shared_rank(part, r) + at * T::kPitch + lane * kVec);
+              y[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, r) + at * T::kPitch + col);
               z[r] = *(cluster.map_shared_rank(sums, r) + at);
             }
           const float before = top;
@@ -684,25 +683,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float old = before == top ? 1.f : ex2((before - top) * a.scale2);
           sum *= old;
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) x[j] *= old;
+          for (int j = 0; j < 4; ++j) x[j] *= old;
 #pragma unroll
           for (int r = 0; r < kMaxSplit; ++r)
             if (r < split) {
               const float f = z[r].x == top ? 1.f : ex2((z[r].x - top) * a.scale2);
               sum += z[r].y * f;
-#pragma unroll
-              for (int j = 0; j < kVec; ++j) x[j] += reinterpret_cast<const float*>(&y[r])[j] * f;
+              x[0] += y[r].x * f;
+              x[1] += y[r].y * f;
+              x[2] += y[r].z * f;
+              x[3] += y[r].w * f;
             }
         }
         const float inv = 1.f / sum;
-        uint16_t* dst = a.out + (long long)(it.q0 + t) * a.out_token +
-                        (long long)(it.head * a.G + i % a.G) * a.out_head + lane * kVec;
-#pragma unroll
-        for (int j = 0; j < kVec; j += 2)
-          *reinterpret_cast<uint32_t*>(dst + j) = seen > 0 ? pack2<BF16>(x[j] * inv, x[j + 1] * inv) : 0;
-        if (a.lse && lane == 0)
-          a.lse[(long long)(it.q0 + t) * a.Hq + it.head * a.G + i % a.G] =
-              seen > 0 ? (top == -INFINITY ? 0.f : top * a.scale) + logf(sum) : -INFINITY;
+        const long long at = it.q0 + t;
+        const int head = it.head * a.G + i % a.G;
+        *reinterpret_cast<uint2*>(a.out + at * a.out_token + head * a.out_head + col) =
+            seen > 0 ? make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv))
+                     : make_uint2(0, 0);
+        if (a.lse && col == 0)
+          a.lse[at * a.Hq + head] = seen > 0 ? (top == -INFINITY ? 0.f : top * a.scale) + logf(sum) : -INFINITY;
       }
     }
     cluster.sync();                                     // no CTA leaves while another reads its part
