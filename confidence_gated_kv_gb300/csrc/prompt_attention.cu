@@ -47,6 +47,22 @@ constexpr int kRows = 128;               // score rows per tile
 constexpr int kKeys = 128;               // keys per tile
 constexpr int kThreads = 384;            // two softmax warpgroups, one for copies and products
 
+// Weights in the inputs' type: exp2(scores - reference + kLift).  The
+// reference moves when a score passes it by more than kLag bits, so a weight
+// stays below 2^(kLift + kLag).  bf16 has the exponents of fp32.  fp16 ends at
+// 2^-24: unlifted, a weight 17 nats below the row's largest one is zero, and
+// with it thousands of keys behind a dominating one.  Lifted by 11 bits it
+// keeps all of its own down to 17 nats and is off by at most 2^-36 of the
+// largest weight below; 2^15 leaves a factor of two to the end of the type.
+// The closer reference costs rescalings (fp16, 16384 tokens of 40 heads:
+// 1828 us with a lift of 7 and a lag of 8, 1865 with 11 and 4, 1896 with 13
+// and 2).
+template <bool BF16>
+struct Weights {
+  static constexpr float kLift = BF16 ? 0.f : 11.f, kLag = BF16 ? 8.f : 4.f;
+  static constexpr float kUnlift = BF16 ? 1.f : 1.f / 2048.f;      // 2^-kLift
+};
+
 constexpr int kRegs = 168;               // registers a thread at launch: 65536 / 384, in eights
 constexpr int kSMs = 152;
 constexpr int kMaxSplit = 8;             // CTAs of a cluster that share an item
@@ -183,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                             const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args a) {
   using T = Tile<D, SPLIT>;
+  using W = Weights<BF16>;
   constexpr int kBytes = T::kBytes, kStages = T::kStages;
   constexpr int kHalf = kRows * 128;                    // one 64-channel column block of a tile
   constexpr uint32_t kTmem = 512, kOut = 256;           // scores at 0 and 128, outputs from 256
@@ -532,11 +549,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c + 32 < kKeys) wait_ld32(s + c + 32);
         }
         const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-        // The reference moves only when it would be passed by more than 2^8:
-        // the weights then stay below 2^8, and the accumulator in tensor
-        // memory is rarely rescaled.  The product that reads it is done:
-        // the scores of this tile were issued after it.
-        const bool move = valid && ((top - ref) * a.scale2 > 8.f || ref == -INFINITY);
+        // The reference moves only when it would be passed by more than
+        // 2^kLag, so that the accumulator in tensor memory is rarely
+        // rescaled.  The product that reads it is done: the scores of this
+        // tile were issued after it.
+        const bool move = valid && ((top - ref) * a.scale2 > W::kLag || ref == -INFINITY);
         if (__any_sync(0xffffffffu, move && j > 0 && top > ref)) {
           const float f = move && top > ref ? ex2((ref - top) * a.scale2) : 1.f;
           l *= f;
@@ -551,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (move) ref = top;
-        const float base = ref == -INFINITY ? 0.f : -ref * a.scale2;
+        const float base = ref == -INFINITY ? 0.f : fmaf(-ref, a.scale2, W::kLift);
         const Pair scale_pair(a.scale2, a.scale2), base_pair(base, base);
         Pair sum[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
 #pragma unroll
@@ -584,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dst = a.out + at * a.out_token + head * a.out_head;
         inv = seen > 0 ? 1.f / l : 0.f;
         if (a.lse)
-          a.lse[at * a.Hq + head] = seen > 0 ? (ref == -INFINITY ? 0.f : ref * a.scale) + logf(l) : -INFINITY;
+          a.lse[at * a.Hq + head] =
+              seen > 0 ? (ref == -INFINITY ? 0.f : ref * a.scale) + logf(l * W::kUnlift) : -INFINITY;
       }
       if (nw > 0) {
         ok = all(o_full(w), items & 1);
@@ -702,7 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             seen > 0 ? make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv))
                      : make_uint2(0, 0);
         if (a.lse && col == 0)
-          a.lse[at * a.Hq + head] = seen > 0 ? (top == -INFINITY ? 0.f : top * a.scale) + logf(sum) : -INFINITY;
+          a.lse[at * a.Hq + head] =
+              seen > 0 ? (top == -INFINITY ? 0.f : top * a.scale) + logf(sum * W::kUnlift) : -INFINITY;
       }
     }
     cluster.sync();                                     // no CTA leaves while another reads its part

@@ -527,7 +527,9 @@ int confkv_rotary_frequencies(int32_t rot, double base, int32_t scaling, double 
  *   [0, total] are clamped to it.  Rows of out and lse that belong to no
  *   sequence are not written.  total_q, total_k < 2^31 - 4096.
  * Scores, maxima, sums and the accumulated output are fp32; the weights are
- * rounded to `dtype` for the product with v, the output once at the end.
+ * rounded to `dtype` for the product with v (fp16: a weight less than 2^-25 of
+ * the row's largest is off by up to 2^-36 of that one instead of 2^-11 of
+ * itself), the output once at the end.
  * Values of keys that no query of the call sees do not reach the output,
  * NaN and infinities among them; a non-finite value of v within a sequence
  * may reach rows up to 127 keys before it.  out must not overlap an input.

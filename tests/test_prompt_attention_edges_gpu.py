@@ -1,0 +1,87 @@
+"""Packed prompt attention where the weights of a row lie far apart, against
+attention in float64.
+
+Tolerance: that of test_prompt_attention_gpu.py, and for fp16 the smallest
+step of a weight.  A weight is held in fp16 relative to a reference that is at
+most the row's largest score, 2^11 at the reference, so its error is at most
+half a step, 2^-25 of 2^11 (and at most u of the weight itself): a row may be
+off by 2^-36 p_max sum_j |v_j| more.
+"""
+import math
+
+import pytest
+import torch
+
+import confidence_gated_kv_gb300 as ck
+
+from test_prompt_attention_gpu import BF16, F16, cu, reference
+
+pytestmark = pytest.mark.gpu
+
+
+def sink_and_tail(n, Hkv, d, dtype, gap, spread, seed):
+    """Keys and values of a sequence whose first key is `gap` nats above all
+    others for the queries of sink_queries, and has a value of zero."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = torch.zeros((n, Hkv, d), device="cuda")
+    k[:, :, 0] = spread * torch.rand((n, Hkv), generator=g, device="cuda")
+    k[0, :, 0] = gap
+    v = 1000.0 + 100.0 * torch.randn((n, Hkv, d), generator=g, device="cuda")
+    v[0] = 0.0
+    return k.to(dtype), v.to(dtype)
+
+
+def sink_queries(rows, Hq, d, dtype):
+    q = torch.zeros((rows, Hq, d), device="cuda")
+    q[:, :, 0] = 4.0                           # times scale 1/4: the score is the key's first channel
+    return q.to(dtype)
+
+
+def check_rows(out, lse, q, k, v, rows):
+    """The first `rows` rows of a call without the causal mask."""
+    ref, tol, rl, ltol = reference(q[:rows], k, v, [rows], [len(k)], False, 0.25)
+    if q.dtype == F16:
+        s = torch.einsum("qhd,khd->qhk", q[:rows].double(),
+                         k.double().repeat_interleave(q.shape[1] // k.shape[1], 1)) * 0.25
+        p_max = torch.exp(s.amax(-1) - rl)
+        total = v.double().abs().sum(0).repeat_interleave(q.shape[1] // k.shape[1], 0)
+        tol = tol + 2.0 ** -36 * p_max[..., None] * total
+    err = (out[:rows].double() - ref).abs()
+    assert torch.isfinite(out).all()
+    assert float((err - tol).max()) <= 0, "off by %.3g of %.3g" % (float(err.max()), float(ref.abs().max()))
+    assert bool(((lse[:rows].double() - rl).abs() <= ltol).all())
+    assert ck.prompt_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+@pytest.mark.parametrize("gap", [10.0, 14.0, 16.0, 17.5, 20.0])
+@pytest.mark.parametrize("rows, Hq, Hkv, n", [
+    (1, 2, 1, 16384),            # keys split over a cluster
+    (4864, 8, 8, 4096),          # whole items
+])
+def test_a_dominating_key_without_value(rows, Hq, Hkv, n, gap, spread, d, dtype):
+    k, v = sink_and_tail(n, Hkv, d, dtype, gap, spread, 1)
+    q = sink_queries(rows, Hq, d, dtype)
+    out, lse = ck.prompt_attention(q, k, v, cu([rows]), cu([n]), causal=False, scale=0.25, return_lse=True)
+    check_rows(out, lse, q, k, v, min(rows, 64))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("step", [0.5, 2.7, 2.9, 6.0])
+def test_a_reference_that_moves_after_the_tail(step, d):
+    # the dominating key comes last, reached over keys that rise by `step`
+    # nats a tile: below and above the distance at which the reference moves
+    n = 4096
+    for rows, Hq, Hkv in ((1, 2, 1), (4864, 8, 8)):
+        k, v = sink_and_tail(n, Hkv, d, F16, 0.0, 0.0, 2)
+        k[:, :, 0] = -15.0
+        rise = min(10, int(15 / step))
+        for i in range(rise):
+            k[128 * (20 + i), :, 0] = -15.0 + step * (i + 1)
+            v[128 * (20 + i)] = 0.0
+        k[n - 1, :, 0], v[n - 1] = 1.0, 0.0
+        q = sink_queries(rows, Hq, d, F16)
+        out, lse = ck.prompt_attention(q, k, v, cu([rows]), cu([n]), causal=False, scale=0.25, return_lse=True)
+        check_rows(out, lse, q, k, v, min(rows, 64))
