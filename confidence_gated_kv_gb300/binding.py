@@ -121,6 +121,7 @@ def lib() -> ctypes.CDLL:
             "confkv_qk_rotary": (ctypes.c_int, [vp, vp]),
             "confkv_prompt_attention": (ctypes.c_int, [vp, vp]),
             "confkv_prompt_status": (ctypes.c_int, [ctypes.POINTER(i32), vp]),
+            "confkv_selftest_prompt_timeout": (ctypes.c_int, [vp, vp]),
             "confkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "confkv_version": (i32, []),
         }

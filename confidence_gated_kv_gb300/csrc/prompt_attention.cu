@@ -91,6 +91,8 @@ struct Args {
   float* lse;
   float scale, scale2;                   // scale2 = scale * log2(e)
   int wide;                              // rows of out start on 32-byte boundaries
+  int absent;                            // CTA whose softmax warps do nothing (self-test), or -1
+  long long limit;                       // cycles after which a wait gives up
 };
 
 struct Item {                            // what one CTA computes
@@ -180,15 +182,17 @@ __device__ __forceinline__ bool find_item(const Args& a, int tile, int head, int
 
 __device__ int32_t g_prompt_status;      // one word per device: a bounded wait gave up
 
-// Bounded wait (about four seconds); false once it, or another wait of the
-// CTA, has given up.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+constexpr long long kWaitLimit = 1LL << 33;     // about four seconds
+constexpr long long kTestLimit = 1LL << 20;     // of the self-test: half a millisecond
+
+// Bounded wait; false once it, or another wait of the CTA, has given up.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, long long limit) {
   if (bar_try(bar, parity)) return true;
   const long long start = clock64();
   do {
     if (bar_try(bar, parity)) return true;
     if (*abort) return false;
-  } while (clock64() - start < (1LL << 33));
+  } while (clock64() - start < limit);
   *abort = 1;
   atomicOr(&g_prompt_status, kStatusTimeout);
   return false;
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = s_tmem;
 
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_on(bar, parity, &s_abort); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_on(bar, parity, &s_abort, a.limit); };
   auto all = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(bar, parity)); };
   // Item k of this CTA, by a whole warp; false at the end of the work.
   auto get_item = [&](int k, Item& it) {
@@ -282,6 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) bar_arrive(item_empty(k));
     return it.found != 0;
+  };
+  // Every role ends here before it looks at s_abort: whichever wait gave up,
+  // all of them then see it, and wait for what they still have in flight.
+  auto leave = [&] {
+    __syncwarp();
+    bar_sync<1>(kThreads);
   };
   float ref = -INFINITY, l = 0.f;                       // softmax threads: the latest item's row
   bool in_item = false;
@@ -385,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tiles += nw;
         items += nw > 0;
       }
+      leave();
       if (s_abort && elect()) {                         // nothing in flight when the CTA ends
         mma_commit(drained(w));
         bar_wait(drained(w), 0);
@@ -431,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
+      leave();
       if (s_abort && lane == 0) {
         for (int w = 0; w < 2; ++w)
           if (queries[w]) bar_wait(q_full(w), (queries[w] - 1) & 1);
@@ -496,13 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) bar_arrive(full(s));
         }
       }
+      leave();
     }
     // All warps go on with the launch's register count.  The softmax warps
-    // give theirs back first: without the barrier, warps that have nothing to
-    // do could take registers that a softmax warpgroup has yet to ask for,
-    // and both would wait for ever.
+    // give theirs back before they leave: without that barrier, warps that
+    // have nothing to do could take registers that a softmax warpgroup has
+    // yet to ask for, and both would wait for ever.
     __syncwarp();
-    bar_sync<1>(kThreads);
     regs_inc<kRegs>();
   } else {
     // ------------------------------------------------------------ softmax
@@ -511,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
     const uint32_t ts = tmem + w * kKeys + lane_base, to = tmem + kOut + w * D + lane_base;
     uint32_t tiles = 0, items = 0;                      // done by this warpgroup: parities of its barriers
-    bool ok = true;
+    bool ok = (int)blockIdx.x != a.absent;
     Item it;
     for (int k = 0; ok && get_item(k, it); ++k) {
       const int nw = w ? it.n1 : it.n0;                 // key tiles of this row tile
@@ -641,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     regs_dec<kRegs>();
-    bar_sync<1>(kThreads);
+    leave();
   }
 
   if (SPLIT) {
@@ -854,7 +866,8 @@ bool rows_apart(const int64_t* stride, int d, long long tokens, long long heads)
 
 using namespace confkv;
 
-extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream) {
+// test: the call of the self-test.
+static int prompt_attention(const confkv_prompt_args* p, bool test, void* stream) {
   if (!p) return CONFKV_EINVAL;
   if (p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->total_q < 0 || p->total_k < 0) return CONFKV_EINVAL;
   constexpr int32_t most = INT32_MAX - 4096;             // a tile's end behind the last row fits 32 bits
@@ -885,6 +898,7 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
   a.lse = p->lse;
   a.scale = p->scale;
   a.scale2 = p->scale * 1.4426950408889634f;
+  a.limit = test ? kTestLimit : kWaitLimit;
   // no more tiles than these, whatever the lengths
   const int per = 2 * a.tokens;
   const long long tiles = p->B == 1 ? (p->total_q + per - 1LL) / per : (long long)p->total_q / per + p->B;
@@ -906,12 +920,23 @@ extern "C" int confkv_prompt_attention(const confkv_prompt_args* p, void* stream
   const Plan plan = plan_items(tiles * p->Hkv, (double)p->total_k / p->B / kKeys);
   auto fn = p->d == 128 ? (bf16 ? launch<128, true> : launch<128, false>)
                         : (bf16 ? launch<64, true> : launch<64, false>);
+  // The last CTA that shares the first item: it has a key tile if any has.
+  a.absent = test ? plan.split - 1 : -1;
   a.split = plan.split;
   const int first = fn(mq, mk, mv, a, plan.whole, st);
   if (first != CONFKV_OK || plan.rest == 0) return first;
   a.item0 = (int)plan.whole;
+  a.absent = -1;
   a.split = plan.rest_split;
   return fn(mq, mk, mv, a, plan.rest, st);
+}
+
+extern "C" int confkv_prompt_attention(const confkv_prompt_args* args, void* stream) {
+  return prompt_attention(args, false, stream);
+}
+
+extern "C" int confkv_selftest_prompt_timeout(const confkv_prompt_args* args, void* stream) {
+  return prompt_attention(args, true, stream);
 }
 
 extern "C" int confkv_prompt_status(int32_t* bits, void* stream) {

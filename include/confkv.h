@@ -557,9 +557,18 @@ int confkv_prompt_attention(const confkv_prompt_args* args, void* stream);
 
 /* Whether a bounded wait of a confkv_prompt_attention kernel gave up on the
  * current device since the last call (CONFKV_STATUS_TIMEOUT in `bits`, and
- * CONFKV_EDEVICE): outputs of the calls since then are not valid.
+ * CONFKV_EDEVICE): outputs of the calls since then are not valid (rows are
+ * unwritten).  The calls themselves are asynchronous and do not report it.
  * Synchronises `stream` and clears the word. */
 int confkv_prompt_status(int32_t* bits, void* stream);
+
+/* Self-test of failure detection: confkv_prompt_attention with one CTA of the
+ * first sequence's last rows (which have to see a key) whose softmax warps do
+ * nothing, and waits that give up after 2^20 cycles.  The CTA's other warps
+ * run into that limit, set the bit above, wait for their copies and products
+ * in flight and leave; nothing faults, and the next call works as ever.
+ * Asynchronous on `stream`. */
+int confkv_selftest_prompt_timeout(const confkv_prompt_args* args, void* stream);
 
 /* Human-readable text of a status code. */
 const char* confkv_status_string(int status);

@@ -1,5 +1,5 @@
-"""Packed prompt attention where the weights of a row lie far apart, against
-attention in float64.
+"""Packed prompt attention at its edges: weights of a row that lie far apart,
+against attention in float64; waits that run out.
 
 Tolerance: that of test_prompt_attention_gpu.py, and for fp16 the smallest
 step of a weight.  A weight is held in fp16 relative to a reference that is at
@@ -7,14 +7,14 @@ most the row's largest score, 2^11 at the reference, so its error is at most
 half a step, 2^-25 of 2^11 (and at most u of the weight itself): a row may be
 off by 2^-36 p_max sum_j |v_j| more.
 """
-import math
 
 import pytest
 import torch
 
 import confidence_gated_kv_gb300 as ck
+from confidence_gated_kv_gb300 import binding, prompt
 
-from test_prompt_attention_gpu import BF16, F16, cu, reference
+from test_prompt_attention_gpu import BF16, F16, cu, inputs, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,32 @@ def test_a_reference_that_moves_after_the_tail(step, d):
         q = sink_queries(rows, Hq, d, F16)
         out, lse = ck.prompt_attention(q, k, v, cu([rows]), cu([n]), causal=False, scale=0.25, return_lse=True)
         check_rows(out, lse, q, k, v, min(rows, 64))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lq, lk, Hq, Hkv", [
+    ([256] * 80, [256] * 80, 8, 8),               # whole items: copies of an item and of the next one in flight
+    ([1400] * 16, [1400] * 16, 8, 8),             # copies that wait for room
+])
+def test_waits_that_run_out_are_reported(lq, lk, Hq, Hkv, d):
+    # a CTA without its softmax: its other warps give up after half a
+    # millisecond.  Rows are right, unwritten, or NaN where a part is missing.
+    (q, k, v), n = inputs(lq, lk, Hq, Hkv, d, F16, 41), sum(lq)
+    cq, ck_ = cu(lq), cu(lk)
+    want = ck.prompt_attention(q, k, v, cq, ck_)
+    assert ck.prompt_status() == 0
+    big = torch.full((n + 16, Hq, d), 7.0, dtype=F16, device="cuda")
+    out = big[8:8 + n]
+    args = prompt._PROMPT.pack(len(lq), Hq, Hkv, d, 0, 1, n, sum(lk), d ** -0.5, q.data_ptr(), k.data_ptr(),
+                               v.data_ptr(), out.data_ptr(), 0, cq.data_ptr(), ck_.data_ptr(), Hq * d, d, Hkv * d, d,
+                               Hkv * d, d, Hq * d, d)
+    assert ck.lib().confkv_selftest_prompt_timeout(args, torch.cuda.current_stream().cuda_stream) == 0
+    assert ck.prompt_status() == binding.STATUS_TIMEOUT
+    assert ck.prompt_status() == 0
+    right = (out == want).all(-1)
+    lost = (out == 7.0).all(-1) | out.isnan().all(-1)
+    assert bool((right | lost).all()) and bool(lost.any()) and bool(right.any())
+    assert bool((big[:8] == 7).all()) and bool((big[8 + n:] == 7).all())
+    for _ in range(3):
+        assert torch.equal(ck.prompt_attention(q, k, v, cq, ck_), want)
+    assert ck.prompt_status() == 0
