@@ -666,6 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Item it = s_item[0];
     __syncthreads();                                    // the products of both row tiles are done
     const bool done = it.found != 0 && !s_abort;
+    // A CTA that gave up left no part: the rows become NaN for those that
+    // would add it.
+    if (threadIdx.x < 2 * kRows && it.found != 0 && s_abort) sums[threadIdx.x] = make_float2(-INFINITY, NAN);
     if (threadIdx.x < 2 * kRows && in_item && done) {
       const int w = warp >> 2, nw = w ? it.n1 : it.n0;
       sums[threadIdx.x] = make_float2(ref, l);

@@ -558,7 +558,8 @@ int confkv_prompt_attention(const confkv_prompt_args* args, void* stream);
 /* Whether a bounded wait of a confkv_prompt_attention kernel gave up on the
  * current device since the last call (CONFKV_STATUS_TIMEOUT in `bits`, and
  * CONFKV_EDEVICE): outputs of the calls since then are not valid (rows are
- * unwritten).  The calls themselves are asynchronous and do not report it.
+ * unwritten, or NaN where only a part of their keys was lost).  The calls
+ * themselves are asynchronous and do not report it.
  * Synchronises `stream` and clears the word. */
 int confkv_prompt_status(int32_t* bits, void* stream);
 

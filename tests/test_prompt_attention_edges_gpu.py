@@ -91,6 +91,8 @@ def test_a_reference_that_moves_after_the_tail(step, d):
 @pytest.mark.parametrize("lq, lk, Hq, Hkv", [
     ([256] * 80, [256] * 80, 8, 8),               # whole items: copies of an item and of the next one in flight
     ([1400] * 16, [1400] * 16, 8, 8),             # copies that wait for room
+    ([1, 1, 1], [3000, 40, 900], 10, 2),          # keys split: the other CTAs of the cluster go on to the merge
+    ([300, 2], [301, 2000], 4, 2),
 ])
 def test_waits_that_run_out_are_reported(lq, lk, Hq, Hkv, d):
     # a CTA without its softmax: its other warps give up after half a
