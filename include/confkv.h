@@ -531,8 +531,10 @@ int confkv_rotary_frequencies(int32_t rot, double base, int32_t scaling, double 
  * the row's largest is off by up to 2^-36 of that one instead of 2^-11 of
  * itself), the output once at the end.
  * Values of keys that no query of the call sees do not reach the output,
- * NaN and infinities among them; a non-finite value of v within a sequence
- * may reach rows up to 127 keys before it.  out must not overlap an input.
+ * NaN and infinities among them.  Within a sequence a non-finite value of v may
+ * also reach rows that do not see it (a weight of zero times infinity): those
+ * whose own last key is at most 126 + floor(128 / G) keys before it.  out must
+ * not overlap an input.
  * The keys of few rows are split over a cluster of CTAs and joined, by a rule
  * on the sizes above: the same call gives the same bits every time, but a
  * sequence's last bits may depend on the sizes of the call it is part of.

@@ -116,3 +116,28 @@ def test_waits_that_run_out_are_reported(lq, lk, Hq, Hkv, d):
     for _ in range(3):
         assert torch.equal(ck.prompt_attention(q, k, v, cq, ck_), want)
     assert ck.prompt_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Hq, Hkv, lq, lk, keys", [
+    (4, 4, [900], [937], [0, 300, 511, 640, 936]),        # a token a row, queries off the tiles' start
+    (10, 2, [900], [900], [255, 256, 899]),               # 25 tokens a tile
+    (8, 8, [2600] * 8, [2600] * 8, [1283, 2500]),         # whole items
+    (3, 1, [5, 40], [1000, 77], [960, 998]),              # keys split over a cluster
+])
+def test_reach_of_a_value_that_is_not_finite(Hq, Hkv, lq, lk, keys, bad):
+    # a tile's rows share its keys, down to those that only its last token
+    # sees: at most 126 + 128 / G keys behind a row's own last one
+    G, d = Hq // Hkv, 64
+    q, k, v = inputs(lq, lk, Hq, Hkv, d, BF16, 51)
+    cq, ck_ = cu(lq), cu(lk)
+    want = ck.prompt_attention(q, k, v, cq, ck_)
+    seen = torch.arange(lq[0], device="cuda") + lk[0] - lq[0]              # last key of each row
+    for key in keys:
+        x = v.clone()
+        x[key, 0, 7] = bad
+        got = ck.prompt_attention(q, k, x, cq, ck_)
+        touched = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+        touched[:lq[0], :G, 7] = (seen + 126 + 128 // G >= key)[:, None]
+        assert torch.equal(got[~touched], want[~touched])
+        assert not bool(torch.isfinite(got[:lq[0], :G, 7][seen >= key]).any())
