@@ -141,3 +141,27 @@ def test_reach_of_a_value_that_is_not_finite(Hq, Hkv, lq, lk, keys, bad):
         touched[:lq[0], :G, 7] = (seen + 126 + 128 // G >= key)[:, None]
         assert torch.equal(got[~touched], want[~touched])
         assert not bool(torch.isfinite(got[:lq[0], :G, 7][seen >= key]).any())
+
+
+@pytest.mark.parametrize("Hq, Hkv", [(4, 2), (40, 8)])
+@pytest.mark.parametrize("n", [100, 6000])
+def test_bad_offsets_write_only_rows_of_sequences(n, Hq, Hkv):
+    # offsets are clamped to [0, n] and a sequence whose end lies before its
+    # start is empty: nothing but the rows of the rest is written, in the
+    # tensors or around them.  100 rows: keys split; 6000: whole items.
+    d, guard = 64, 40
+    q, k, v = inputs([n], [n], Hq, Hkv, d, F16, 61)
+    for offsets in ([0, n + 4900], [-7, n - 40, 30, n], [50, 20, 1 << 30], [90, 90, 90], [-(1 << 31), -5], [n, n + 9],
+                    [0, 40, -3, -2]):
+        out = torch.full((n + 2 * guard, Hq, d), 7.0, dtype=F16, device="cuda")
+        lse = torch.full((n + 2 * guard, Hq), 7.0, device="cuda")
+        c = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        ck.prompt_attention(q, k, v, c, out=out[guard:guard + n], lse=lse[guard:guard + n])
+        written = torch.zeros(n + 2 * guard, dtype=torch.bool, device="cuda")
+        for a, b in zip(offsets, offsets[1:]):
+            a, b = min(max(a, 0), n), min(max(b, 0), n)
+            written[guard + a:guard + max(a, b)] = True
+        assert bool((out[~written] == 7).all()) and bool((lse[~written] == 7).all())
+        if sorted(offsets) == offsets:                    # every row of a sequence
+            assert not bool((out[written] == 7).all(-1).any()) and not bool((lse[written] == 7).any())
+    assert ck.prompt_status() == 0
