@@ -209,6 +209,21 @@ def allocating_on(stream):
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
+def used_on(stream, *tensors):
+    """Tells the allocator that work queued on `stream` (None: the current
+    one, nothing to tell) reads or writes `tensors`: their memory is not handed
+    out again before that work is done.  Not told of a stream that torch does
+    not own (a raw handle, an ExternalStream): the allocator would use it when
+    the tensors are freed, and it may be gone by then."""
+    if stream is None:
+        return
+    import torch
+    if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 _raw_stream_fn = None
 
 
@@ -325,6 +340,7 @@ class Cache:
             raise ValueError("prefill_len: one length per sequence is wanted")
         call_on(self._dev_index, lib().confkv_prefill_begin, "confkv_prefill_begin",
                 (self._h, struct.pack("=%di" % self.B, *prefill_len)), stream)
+        used_on(stream, self.workspace)
         self._prompt_rows = sum(prefill_len)
 
     def _packed(self, t, name, rows):
@@ -349,6 +365,7 @@ class Cache:
             raise ValueError("k and v: one type is wanted")
         call_on(self._dev_index, lib().confkv_prefill_layer, "confkv_prefill_layer",
                 (self._h, layer, k_at, v_at, dtype_code(k.dtype), ks, vs), stream)
+        used_on(stream, k, v, self.workspace)
 
     def read_rows(self) -> int:
         """Rows that always hold a layer's resident entries (exact until the
@@ -385,6 +402,7 @@ class Cache:
                     raise ValueError("%s: a contiguous int32 vector of %d on the cache's device is wanted" % (name, n))
         call_on(self._dev_index, lib().confkv_read_layer, "confkv_read_layer",
                 (self._h, layer, dtype_code(k.dtype), k_at, v_at, ks, vs, pos.data_ptr(), cu.data_ptr(), rows), stream)
+        used_on(stream, k, v, pos, cu, self.workspace)
         return out
 
     def new_outputs(self):

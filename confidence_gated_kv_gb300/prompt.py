@@ -3,13 +3,19 @@ prompt attention (include/confkv.h: confkv_qk_rotary, confkv_prompt_attention).
 
 Argument marshalling only, as in binding.py; layer-wise prefill and read-back
 of a cache are methods of Cache.
+
+Calls run on `stream`, or on the current stream when it is None.  With a
+torch.cuda.Stream, tensors may be freed as soon as the call returns; with a
+raw handle or an ExternalStream the caller keeps them until the stream has
+done the work.  New outputs belong to `stream`: another stream waits for it
+before it uses them.
 """
 from __future__ import annotations
 
 import ctypes
 import struct
 
-from .binding import FP32, _check, _stream, allocating_on, call_on, dtype_code, lib
+from .binding import FP32, _check, _stream, allocating_on, call_on, dtype_code, lib, used_on
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -151,6 +157,9 @@ def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float 
                         k_at, q_out.data_ptr(), ko_at, qs[0], qs[1], ks[0], ks[1], qos[0], qos[1], kos[0], kos[1],
                         qw_at, kw_at, pos_at, turns_at)
     call_on(dev, lib().confkv_qk_rotary, "confkv_qk_rotary", (args,), stream)
+    if stream is not None:
+        used_on(stream, q, k, q_out, k_out, q_weight, k_weight, positions if rot else None,
+                rotary.turns if rot else None)
     return q_out, k_out
 
 
@@ -197,6 +206,7 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
                         d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                         out.data_ptr(), lse_at, cu_at, cuk_at, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1])
     call_on(dev, lib().confkv_prompt_attention, "confkv_prompt_attention", (args,), stream)
+    used_on(stream, q, k, v, cu_seqlens, cu_seqlens_k, out, lse)
     return (out, lse) if return_lse else out
 
 

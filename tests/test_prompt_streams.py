@@ -1,0 +1,139 @@
+"""Prompt operators on a given stream: whose memory has to outlive the call.
+
+On the CPU with stand-ins for tensors and streams (nothing is launched); on a
+GPU with inputs that are freed, and their memory written, while the stream is
+still busy with other work."""
+import pytest
+import torch
+
+import confidence_gated_kv_gb300 as ck
+from confidence_gated_kv_gb300 import binding, prompt
+
+
+class Stream:
+    cuda_stream = 1 << 20
+
+
+class External(Stream):
+    pass
+
+
+class Tensor:
+    """What the bindings ask of a contiguous CUDA tensor."""
+    is_cuda, requires_grad, device = True, False, torch.device("cuda", 0)
+
+    def __init__(self, *shape, dtype=torch.float16):
+        self.shape, self.dtype, self.used_on = torch.Size(shape), dtype, []
+
+    def stride(self):
+        s = [1]
+        for n in self.shape[:0:-1]:
+            s.insert(0, s[0] * n)
+        return tuple(s)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def __len__(self):
+        return self.shape[0]
+
+    def record_stream(self, s):
+        self.used_on.append(s)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names of the library calls, none of which is made."""
+    names = []
+    for module in (binding, prompt):
+        monkeypatch.setattr(module, "call_on", lambda index, fn, name, args, stream: names.append(name))
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    prompt._bind()
+    return names
+
+
+def every_call(stream):
+    """Each call with a stream, and the tensors that the work reads or writes."""
+    i32 = lambda *s: Tensor(*s, dtype=torch.int32)  # noqa: E731
+    q, k, v, out, cu, cuk = Tensor(9, 4, 64), Tensor(9, 2, 64), Tensor(9, 2, 64), Tensor(9, 4, 64), i32(2), i32(2)
+    lse = Tensor(9, 4, dtype=torch.float32)
+    ck.prompt_attention(q, k, v, cu, cuk, out=out, lse=lse, stream=stream)
+    yield "attention", [q, k, v, out, cu, cuk, lse]
+    rotary = ck.Rotary(64, device="cpu")
+    rotary.turns, rotary.device_index = Tensor(32, dtype=torch.int64), 0
+    q, k, qo, ko, pos = Tensor(9, 4, 64), Tensor(9, 2, 64), Tensor(9, 4, 64), Tensor(9, 2, 64), i32(9)
+    qw, kw = Tensor(64), Tensor(64)
+    ck.qk_rotary(q, k, pos, rotary, qw, kw, q_out=qo, k_out=ko, stream=stream)
+    yield "rotary", [q, k, qo, ko, pos, qw, kw, rotary.turns]
+    c = ck.Cache.__new__(ck.Cache)
+    c._h, c._dev_index, c.B, c.Hkv, c.d, c.workspace = None, 0, 1, 2, 64, Tensor(1)
+    k, v = Tensor(9, 2, 64), Tensor(9, 2, 64)
+    c.prefill_begin([9], stream=stream)
+    yield "begin", [c.workspace]
+    c.workspace = Tensor(1)
+    c.prefill_layer(0, k, v, stream=stream)
+    yield "layer", [k, v, c.workspace]
+    c.workspace = Tensor(1)
+    o = dict(k=Tensor(9, 2, 64), v=Tensor(9, 2, 64), positions=i32(9), cu_seqlens=i32(2))
+    c.read_layer(0, out=o, stream=stream)
+    yield "read", [*o.values(), c.workspace]
+
+
+def test_tensors_are_held_for_a_given_stream(calls):
+    s = Stream()
+    for name, tensors in every_call(s):
+        for i, t in enumerate(tensors):
+            assert t.used_on == [s], (name, i)
+    assert len(calls) == 5
+
+
+@pytest.mark.parametrize("stream", [None, External(), 1 << 20])
+def test_nothing_is_told_of_other_streams(calls, stream):
+    # the current stream needs nothing; one that torch does not own may be gone when the tensors are freed
+    for name, tensors in every_call(stream):
+        assert all(t.used_on == [] for t in tensors), name
+
+
+@pytest.mark.gpu
+def test_inputs_freed_behind_the_call():
+    n, Hq, Hkv, d = 700, 8, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    make = lambda h: torch.randn((n, h, d), generator=g, device="cuda").half()  # noqa: E731
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    keep = make(Hq), make(Hkv), make(Hkv)
+    rotary = ck.Rotary(d)
+    cfg = ck.make_config(L=1, Hq=Hq, Hkv=Hkv, d=d, V=1000, B=1, cap=1024, W=64, P=1, n_high=[1024], n_low=[1024])
+    cache = ck.Cache(cfg)
+
+    def run(q, k, v, stream):
+        """out of every operator, all on `stream`"""
+        a = ck.prompt_attention(q, k, v, cu, stream=stream)
+        b = ck.qk_rotary(q, k, pos, rotary, stream=stream)
+        cache.prefill_begin([n], stream=stream)
+        cache.prefill_layer(0, k, v, stream=stream)
+        r = cache.read_layer(0, stream=stream)
+        return a, *b, r["k"], r["v"]
+
+    want = run(*keep, None)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        q, k, v = (x.clone() for x in keep)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)                     # about 10 ms before the operators start
+        got = run(q, k, v, s)
+        del q, k, v
+        new = [torch.full_like(x, 100.0) for x in keep]       # the freed memory, were it handed out
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        del new
