@@ -200,13 +200,15 @@ def call_on(index: int, fn, name: str, args: tuple, stream):
         _check(status, name)
 
 
-def allocating_on(stream):
-    """Context for new tensors that work on `stream` (None: the current one)
-    will write: memory of the current stream may still be in use there."""
+def allocating_on(stream, index: int):
+    """Context for new tensors on device `index` that work on `stream` (None:
+    the current one) will write: memory of the current stream may still be in
+    use there."""
     if stream is None:
         return _same
     import torch
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
+                             torch.cuda.ExternalStream(int(stream), device=index))
 
 
 def used_on(stream, *tensors):
@@ -382,7 +384,7 @@ class Cache:
         import torch
         if out is None:
             rows, dev, empty = self.read_rows(), self.device, torch.empty
-            with _same if stream is None else allocating_on(stream):
+            with allocating_on(stream, self._dev_index):
                 k = empty((rows, self.Hkv, self.d), dtype=torch.float16 if dtype is None else dtype, device=dev)
                 v = torch.empty_like(k)
                 pos = empty(rows, dtype=torch.int32, device=dev)

@@ -93,7 +93,7 @@ def _like(t, stream):
     on `stream`."""
     if stream is None and t.is_contiguous():
         return torch.empty_like(t)
-    with allocating_on(stream):
+    with allocating_on(stream, t.get_device()):
         return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
@@ -199,7 +199,7 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
             _unfit("lse: a contiguous fp32 [rows, heads] tensor on the device of q is wanted")
         lse_at = lse.data_ptr()
     elif return_lse:
-        with allocating_on(stream):
+        with allocating_on(stream, dev):
             lse = torch.empty((nq, Hq), dtype=torch.float32, device=q.device)
         lse_at = lse.data_ptr()
     args = _PROMPT.pack(B, Hq, Hkv, d, dtype_code(dtype), 1 if causal else 0, nq, nk,

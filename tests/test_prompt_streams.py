@@ -101,6 +101,23 @@ def test_nothing_is_told_of_other_streams(calls, stream):
         assert all(t.used_on == [] for t in tensors), name
 
 
+def test_a_raw_handle_is_a_stream_of_the_tensors_device(monkeypatch):
+    # new outputs on another device than the current one belong to a stream of theirs
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: made.append((handle, device)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: binding._same)
+    with binding.allocating_on(1 << 20, 3):
+        pass
+    assert made == [(1 << 20, 3)]
+    monkeypatch.setattr(prompt, "allocating_on", lambda stream, index: made.append((stream, index)) or binding._same)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: None)
+    t = Tensor(4, 2, 64)
+    t.get_device = lambda: 5
+    prompt._bind()
+    prompt._like(t, 1 << 20)
+    assert made[1] == (1 << 20, 5)
+
+
 @pytest.mark.gpu
 def test_inputs_freed_behind_the_call():
     n, Hq, Hkv, d = 700, 8, 2, 128
@@ -137,3 +154,18 @@ def test_inputs_freed_behind_the_call():
         for x, y in zip(got, want):
             assert torch.equal(x, y)
         del new
+
+
+@pytest.mark.gpu
+def test_raw_handles():
+    q, k, v = (torch.randn(50, h, 64, device="cuda").half() for h in (4, 2, 2))
+    cu = torch.tensor([0, 50], dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    want = ck.prompt_attention(q, k, v, cu, return_lse=True)
+    for handle in (s.cuda_stream, 0):
+        got = ck.prompt_attention(q, k, v, cu, return_lse=True, stream=handle)
+        a = ck.qk_rotary(q, k, None, None, torch.ones(64, device="cuda").half(), stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(a[1], k)
