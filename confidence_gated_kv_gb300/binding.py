@@ -178,6 +178,29 @@ def dtype_code(dtype) -> int:
     return code
 
 
+_forward_ad = None
+
+
+def no_gradients(*tensors):
+    """For operators without derivatives: a result that autograd would treat as
+    a constant is refused rather than computed."""
+    global _forward_ad
+    import torch
+    if _forward_ad is None:
+        from torch.autograd import forward_ad
+        _forward_ad = forward_ad
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("an input requires gradients, which this operator does not give: call it under "
+                                 "torch.no_grad()")
+    if getattr(_forward_ad, "_current_level", 0) >= 0:        # within a dual level, which no_grad() does not end
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("an input has a forward-mode tangent, which this operator does not carry on: call it "
+                                 "with the primal")
+
+
 _same = contextlib.nullcontext()
 _current_device = None
 
@@ -357,7 +380,9 @@ class Cache:
 
     def prefill_layer(self, layer: int, k, v, stream=None):
         """K/V of one layer for all sequences, [rows, Hkv, d] fp16 or bf16, the
-        sequences' rows one after another."""
+        sequences' rows one after another.  What is read back or attended later
+        is a constant for autograd: k and v that require gradients are refused
+        while gradients are enabled, and forward-mode tangents always."""
         rows = getattr(self, "_prompt_rows", None)
         if rows is None:
             raise ConfkvError(ESTATE, "prefill_layer before prefill_begin")
@@ -365,6 +390,7 @@ class Cache:
         v_at, vs = self._packed(v, "v", rows)
         if k.dtype != v.dtype:
             raise ValueError("k and v: one type is wanted")
+        no_gradients(k, v)
         call_on(self._dev_index, lib().confkv_prefill_layer, "confkv_prefill_layer",
                 (self._h, layer, k_at, v_at, dtype_code(k.dtype), ks, vs), stream)
         used_on(stream, k, v, self.workspace)

@@ -15,7 +15,7 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from .binding import FP32, _check, _stream, allocating_on, call_on, dtype_code, lib, used_on
+from .binding import FP32, _check, _stream, allocating_on, call_on, dtype_code, lib, no_gradients, used_on
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -97,27 +97,19 @@ def _like(t, stream):
         return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _no_gradients(*tensors):
-    """The operators have no backward pass: a result that autograd would treat
-    as a constant is refused rather than returned."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                _unfit("an input requires gradients, which this operator does not give: call it under torch.no_grad()")
-
-
 def qk_rotary(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
               stream=None):
     """Per-head RMS norm (where a weight is given) and rotary rotation of
     q [n, Hq, d] and k [n, Hkv, d] at int32 `positions` [n].  `rotary` may be
     None (norms only), k None (queries only).  Returns (q_out, k_out): new
     tensors of the inputs' type, or the given ones, which may be of another
-    type, strided, or the inputs themselves.  No backward pass: inputs that
-    require gradients are refused while gradients are enabled."""
+    type, strided, or the inputs themselves.  No derivatives: inputs that
+    require gradients are refused while gradients are enabled, and inputs with
+    forward-mode tangents always."""
     if torch is None:
         _bind()
     (n, Hq, d), qs = _dims(q, "q")
-    _no_gradients(q, k, q_weight, k_weight)
+    no_gradients(q, k, q_weight, k_weight)
     dev, code = q.get_device(), dtype_code(q.dtype)
     if q_out is None:
         q_out, qo_code, qos = _like(q, stream), code, (Hq * d, d)
@@ -170,14 +162,14 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     device): first query row of each sequence and the end; cu_seqlens_k the
     same for keys (default: cu_seqlens).  With `causal` the queries are the
     last of their sequence's keys.  scale defaults to 1 / sqrt(d).  Returns
-    out, or (out, lse) with return_lse; lse is fp32 [rows, Hq].  No backward
-    pass: inputs that require gradients are refused while gradients are
-    enabled.  A sequence's last bits may depend on the sizes of the whole call:
+    out, or (out, lse) with return_lse; lse is fp32 [rows, Hq].  No
+    derivatives: inputs that require gradients are refused while gradients are
+    enabled, and inputs with forward-mode tangents always.  A sequence's last bits may depend on the sizes of the whole call:
     the keys of few rows are split over more of the GPU and joined."""
     if torch is None:
         _bind()
     (nq, Hq, d), qs = _dims(q, "q")
-    _no_gradients(q, k, v)
+    no_gradients(q, k, v)
     dev, dtype = q.get_device(), q.dtype
     (nk, Hkv, dk), ks = _dims(k, "k", dev)
     shape, vs = _dims(v, "v", dev)
