@@ -23,6 +23,7 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <mutex>
 
 namespace confkv {
 
@@ -216,13 +217,20 @@ constexpr int kMaxDevices = 64;
 
 // Raises `kernel`'s dynamic shared memory limit to at least `bytes` on the
 // current device.  cudaFuncSetAttribute acts on the current device only, so
-// each launcher keeps its own record `done` of the limit set per device.
+// each launcher keeps its own record `done` of the limit set per device.  Calls
+// may come from several threads: without the lock, one that asks for less
+// could set the limit after one that asked for more.
+inline std::mutex& smem_limit_mutex() {
+  static std::mutex m;
+  return m;
+}
 template <typename... KArgs>
 inline cudaError_t ensure_smem(void (*kernel)(KArgs...), int bytes, int (&done)[kMaxDevices]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
+  std::lock_guard<std::mutex> lock(smem_limit_mutex());
   if (known && done[dev] >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && known) done[dev] = bytes;

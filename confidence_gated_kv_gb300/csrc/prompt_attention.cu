@@ -29,7 +29,6 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <mutex>
 
 #include "../../include/confkv.h"
 #include "confkv_internal.cuh"
@@ -780,18 +779,13 @@ bool encode(CUtensorMap* m, const void* p, bool bf16, int d, long long heads, lo
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-std::mutex g_mu;
-
 template <int D, bool BF16, bool SPLIT>
 int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, long long items,
            cudaStream_t st) {
   static int done[kMaxDevices] = {};
   auto kernel = prompt_attention_kernel<D, BF16, SPLIT>;
   constexpr int smem = Tile<D, SPLIT>::kSmem;
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (ensure_smem(kernel, smem, done) != cudaSuccess) return CONFKV_ECUDA;
-  }
+  if (ensure_smem(kernel, smem, done) != cudaSuccess) return CONFKV_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * a.split));
   cfg.blockDim = dim3(kThreads);

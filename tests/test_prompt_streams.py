@@ -3,6 +3,8 @@
 On the CPU with stand-ins for tensors and streams (nothing is launched); on a
 GPU with inputs that are freed, and their memory written, while the stream is
 still busy with other work."""
+import threading
+
 import pytest
 import torch
 
@@ -169,3 +171,39 @@ def test_raw_handles():
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert torch.equal(a[1], k)
+
+
+@pytest.mark.gpu
+def test_two_caches_in_two_threads():
+    # the library's per-device records are shared by all threads
+    lens = [300, 70, 1500]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    data, caches, want = [], [], []
+    for d, H in ((64, 3), (128, 2)):
+        cfg = ck.make_config(L=2, Hq=H, Hkv=H, d=d, V=1000, B=3, cap=1500, W=32, P=1, n_high=[1500] * 2, n_low=[1500] * 2)
+        data.append([torch.randn((sum(lens), H, d), generator=g, device="cuda").half() for _ in range(4)])
+        caches.append(ck.Cache(cfg))
+
+    def work(i, stream, rounds):
+        c, x = caches[i], data[i]
+        for _ in range(rounds):
+            c.prefill_begin(lens, stream=stream)
+            for l in range(2):
+                c.prefill_layer(l, x[2 * l], x[2 * l + 1], stream=stream)
+            got[i] = [c.read_layer(l, stream=stream) for l in range(2)]
+        stream.synchronize()
+
+    got = [None, None]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i, streams[i], 30)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    want, got = got, [None, None]
+    for i in range(2):                                  # the same, one after the other
+        work(i, streams[i], 1)
+        for a, b in zip(want[i], got[i]):
+            assert all(torch.equal(a[key], b[key]) for key in a)
+        assert caches[i].stats()["device_status"] == 0
