@@ -937,6 +937,15 @@ int confkv_import_unit(confkv_ctx* ctx, int32_t b, int32_t l, const confkv_unit_
   cudaStream_t st = as_stream(stream);
   const size_t u0 = unit_index(s, l, b, 0), lb = lb_index(s, l, b);
   int32_t n8 = in->n8;
+  if (!ctx->prefilled) {
+    // The first unit: the others are empty until they are imported, as after
+    // a prefill of nothing.  Kernels index with their counts and positions.
+    const std::vector<int32_t> none(s.B, 0);
+    if (cudaMemsetAsync(ctx->d.T0, 0, s.B * sizeof(int32_t), st) != cudaSuccess) return CONFKV_ECUDA;
+    if (launch_prefill(s, ctx->d, nullptr, nullptr, 0, none.data(), st) != 0) return CONFKV_ECUDA;
+    if (cudaMemcpyAsync(ctx->d.T0, ctx->T0.data(), s.B * sizeof(int32_t), cudaMemcpyHostToDevice, st) != cudaSuccess)
+      return CONFKV_ECUDA;
+  }
   cudaError_t e = cudaMemcpyAsync(ctx->d.k8 + u0 * s.cstride * D, k8.data(), k8.size(), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(ctx->d.v8 + u0 * s.cstride * D, v8.data(), v8.size(), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(ctx->d.k16 + u0 * s.WR * D, k16.data(), k16.size() * 2, cudaMemcpyHostToDevice, st);

@@ -295,7 +295,9 @@ int confkv_export_unit(confkv_ctx* ctx, int32_t b, int32_t l, confkv_unit_host* 
 /* Overwrite the cache of (b, l) from host buffers in the export layout
  * (synchronises `stream`).  FP16 entries go to ring slot pos mod (W + 16);
  * two entries must not share a slot.  Used to resume from a checkpoint or to
- * load a crafted state. */
+ * load a crafted state.  The first import into a context that was not
+ * prefilled empties all other units; its clock is at 0 or where
+ * confkv_set_clock put it. */
 int confkv_import_unit(confkv_ctx* ctx, int32_t b, int32_t l, const confkv_unit_host* in,
                        void* stream);
 
