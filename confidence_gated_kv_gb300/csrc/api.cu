@@ -847,6 +847,7 @@ int confkv_export_unit(confkv_ctx* ctx, int32_t b, int32_t l, confkv_unit_host* 
   if (!o->pos8 || !o->ema8 || !o->k8 || !o->v8 || !o->posR || !o->emaR || !o->k16 || !o->v16 ||
       !o->sK || !o->sV)
     return CONFKV_EINVAL;
+  if (!ctx->prefilled && (ctx->layers_open == 0 || ctx->layer_open[l])) return CONFKV_ESTATE;   // nothing there yet
   const Shape& s = ctx->s;
   const int D = s.D, Hkv = s.Hkv;
   std::vector<uint8_t> k8, v8;

@@ -134,8 +134,9 @@ int confkv_prefill(confkv_ctx* ctx, const int32_t* prefill_len, const void* k, c
  * packed without padding -- so that no layer's K/V has to be kept.
  *   confkv_prefill_begin  resets the cache and fixes the prompt lengths
  *       (HOST array of B).  Until every layer is written the context is not
- *       prefilled: confkv_step, confkv_read_layer, confkv_import_unit and
- *       confkv_set_clock return CONFKV_ESTATE.  CONFKV_ECAPACITY if a length
+ *       prefilled: confkv_step, confkv_read_layer, confkv_import_unit,
+ *       confkv_set_clock and confkv_export_unit of a layer not yet written
+ *       return CONFKV_ESTATE.  CONFKV_ECAPACITY if a length
  *       minus W exceeds cap.
  *   confkv_prefill_layer  writes layer `layer`: k, v device [rows][Hkv][d],
  *       rows = the sum of the lengths, sequence b's rows after those of
@@ -289,7 +290,8 @@ typedef struct confkv_unit_host {
   float* sV;
 } confkv_unit_host;
 
-/* Copy the cache of (b, l) to host (synchronises `stream`). */
+/* Copy the cache of (b, l) to host (synchronises `stream`).  CONFKV_ESTATE
+ * before a prefill, and for a layer that a prefill by layer has yet to write. */
 int confkv_export_unit(confkv_ctx* ctx, int32_t b, int32_t l, confkv_unit_host* out, void* stream);
 
 /* Overwrite the cache of (b, l) from host buffers in the export layout

@@ -1,9 +1,11 @@
 """A context that was never prefilled and holds some imported units: the others
-are empty, whatever the workspace held before."""
+are empty, whatever the workspace held before.  Units that hold nothing yet
+are not exported."""
 import pytest
 import torch
 
 import confidence_gated_kv_gb300 as ck
+from confidence_gated_kv_gb300 import binding
 
 from test_layer_io_gpu import _over, config, packed, padded, same_unit
 
@@ -44,3 +46,27 @@ def test_units_not_imported_are_empty(d, garbage):
         for s in range(2):
             same_unit(part.export_unit(s, l), whole.export_unit(s, l))
     assert part.stats()["device_status"] == 0
+
+
+def test_units_without_content_are_not_exported():
+    lens = [40, 7]
+    cfg = config(lens, 2, 4, 2, 64, 16)
+    ks, vs = packed(lens, 2, 2, 64, torch.float16, 3)
+    cache = ck.Cache(cfg)
+
+    def refused(layer):
+        with pytest.raises(ck.ConfkvError) as e:
+            cache.export_unit(1, layer)
+        return e.value.status == binding.ESTATE
+
+    assert refused(0) and refused(1)
+    cache.prefill_begin(lens)
+    assert refused(0) and refused(1)
+    cache.prefill_layer(1, ks[1], vs[1])
+    first = cache.export_unit(1, 1)
+    assert refused(0)
+    cache.prefill_layer(0, ks[0], vs[0])
+    same_unit(first, cache.export_unit(1, 1))
+    cache.export_unit(1, 0)
+    cache.prefill_begin(lens)
+    assert refused(1)
