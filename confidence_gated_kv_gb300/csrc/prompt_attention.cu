@@ -21,9 +21,9 @@
 // (about 1500 cycles, 700 of them the exponentials) and both products (1024)
 // to the next scores; two of them interleave and keep the tensor cores busy
 // for 70 % of the time.  Measured (bf16, 40 query heads on 8, d = 128): one
-// prompt of 16384 tokens 1.91 ms, 1.44 PFLOP/s; eight prompts of 1 to 2047
-// tokens 99 us; single tokens of eight sequences on 15 216 keys 25 us, with
-// K and V at 5 TB/s while they stream.
+// prompt of 16384 tokens 1.92 ms, 1.43 PFLOP/s; eight prompts of 1 to 2047
+// tokens 99 us; single tokens of eight sequences on 15 216 keys 25 us: every
+// item is split in two, so the longest histories set the time.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -812,7 +812,9 @@ int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, 
 // How the items are launched, from what the host knows: the largest number of
 // items and the average number of key tiles of a sequence.  Time is taken as
 // rounds of the SMs times (key tiles of a CTA + the tiles that its start and
-// its merge take).  A last round with few items can go into a launch of its
+// its merge take: 3, or 4 with a merge, at about 1.7 us each; 2 more for a
+// second launch).  Histories of unlike lengths are not seen: their items get
+// the split of the mean, and the longest of them sets the time.  A last round with few items can go into a launch of its
 // own whose keys are split (160 items of 117 tiles: 323 us with all of them
 // split in two, 251 us as 152 whole ones and 8 split in eight).
 struct Plan {

@@ -36,7 +36,9 @@ class Rotary:
     """Frequencies of a rotary embedding of the first `rot_dim` channels, kept
     on `device` (default: the current one).  scaling: "none", "linear", "ntk"
     or "yarn", for positions beyond the trained `original_length`; the formulas
-    are with confkv_rotary_frequencies."""
+    are with confkv_rotary_frequencies.  "yarn" ramps linearly in the turns of
+    a pair within the trained length, as the paper does; checkpoints tuned with
+    a ramp over the pair index need another table."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                  original_length: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,

@@ -157,10 +157,12 @@ int confkv_prefill_layer(confkv_ctx* ctx, int32_t layer, const void* k, const vo
 /*
  * The resident entries of one layer as packed K/V, dequantised on the device
  * (confkv_export_unit gives codes and scales to the host): for attention of
- * further prompt tokens over a cache, or for handing a sequence on.
+ * further prompt tokens over a cache, or for handing a sequence on.  Entries
+ * of further tokens go into the cache by confkv_step only: a prefill starts it
+ * anew.
  *   k, v       device [rows][Hkv][d], dtype CONFKV_FP16 or CONFKV_BF16:
- *              fp16 window entries converted, INT8 entries code * scale, each
- *              rounded once
+ *              fp16 window entries converted, INT8 entries code * scale in
+ *              fp32, then rounded to dtype
  *   positions  device int32 [rows]: absolute position of each row
  *   cu         device int32 [B + 1], written: sequence b has rows cu[b] ..
  *              cu[b+1]-1, INT8 entries in slot order (by position until the
@@ -469,7 +471,7 @@ int confkv_confidence_noalloc(const float* logits, int32_t B, int32_t V, double 
  * for the pairs of the first rot channels, (2i, 2i + 1) if `interleaved`,
  * else (i, i + rot / 2), with t = 2 pi * position * turns[i] / 2^64.  Channels
  * from rot on are not rotated.  All arithmetic is fp32 (angles exact modulo
- * one turn), rounded once to the output type.
+ * one turn, then rounded to fp32), rounded to the output type at the end.
  *   q [n][Hq][d], k [n][Hkv][d] in in_dtype; q_out, k_out the same shapes in
  *   their own types; any of fp16, bf16, fp32.  Strides in elements, token
  *   first, then head; channels contiguous, addresses aligned to the element.
@@ -504,7 +506,11 @@ int confkv_qk_rotary(const confkv_rotary_args* args, void* stream);
  *   CONFKV_ROTARY_YARN    (arXiv 2309.00071) with r = original_length f_i /
  *       (2 pi) turns in the trained length, g = clamp((r - beta_slow) /
  *       (beta_fast - beta_slow), 0, 1): f_i g + f_i / factor (1 - g), and
- *       mscale = 0.1 ln(factor) + 1 (1 otherwise)
+ *       mscale = 0.1 ln(factor) + 1 (1 otherwise).  The ramp is linear in the
+ *       turns r, as in that paper.  Code that loads such checkpoints commonly
+ *       ramps linearly in the pair index i between rounded bounds, which gives
+ *       other frequencies within the ramp: for those and other rules,
+ *       confkv_qk_rotary takes any table of turns.
  * factor >= 1.  Host only. */
 enum { CONFKV_ROTARY_PLAIN = 0, CONFKV_ROTARY_LINEAR = 1, CONFKV_ROTARY_NTK = 2, CONFKV_ROTARY_YARN = 3 };
 int confkv_rotary_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original_length,
