@@ -814,9 +814,10 @@ int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, 
 // rounds of the SMs times (key tiles of a CTA + the tiles that its start and
 // its merge take: 3, or 4 with a merge, at about 1.7 us each; 2 more for a
 // second launch).  Histories of unlike lengths are not seen: their items get
-// the split of the mean, and the longest of them sets the time.  A last round with few items can go into a launch of its
-// own whose keys are split (160 items of 117 tiles: 323 us with all of them
-// split in two, 251 us as 152 whole ones and 8 split in eight).
+// the split of the mean, and the longest of them sets the time.  A
+// last round with few items can go into a launch of its own whose keys are
+// split (160 items of 117 tiles: 323 us with all of them split in two, 251 us
+// as 152 whole ones and 8 split in eight).
 struct Plan {
   long long whole, rest;                 // items of the first launch, and of one more
   int split, rest_split;

@@ -166,8 +166,9 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True
     last of their sequence's keys.  scale defaults to 1 / sqrt(d).  Returns
     out, or (out, lse) with return_lse; lse is fp32 [rows, Hq].  No
     derivatives: inputs that require gradients are refused while gradients are
-    enabled, and inputs with forward-mode tangents always.  A sequence's last bits may depend on the sizes of the whole call:
-    the keys of few rows are split over more of the GPU and joined."""
+    enabled, and inputs with forward-mode tangents always.  A
+    sequence's last bits may depend on the sizes of the whole call: the keys of
+    few rows are split over more of the GPU and joined."""
     if torch is None:
         _bind()
     (nq, Hq, d), qs = _dims(q, "q")
