@@ -10,6 +10,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cfloat>
 
 #include "confkv_internal.cuh"
 #include "tcgen05.cuh"
@@ -95,6 +96,14 @@ __device__ __forceinline__ float row_factor(float largest) {
 __device__ __forceinline__ float row_unfactor(float largest) {       // its reciprocal
   const int e = min(max((int)(__float_as_uint(largest) >> 23), 14), 254);
   return __uint_as_float((uint32_t)(e - 13) << 23);
+}
+// Log2 units of a row's accumulated products.  Never zero or infinite: hidden
+// keys are -inf in the accumulator, and -inf * 0 or 0 * inf would make the row
+// NaN.  Products stay below 2^40, so a unit below the smallest normal number
+// leaves scores of next to zero either way, and one beyond fp32 has a row of
+// zeros or scores beyond fp32.
+__device__ __forceinline__ float row_unit(const Call& a, float largest) {
+  return fminf(fmaxf(a.scale2 * row_unfactor(largest), FLT_MIN), FLT_MAX);
 }
 // x0, x1 rounded to fp16, and what the rounding left.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {

@@ -87,7 +87,7 @@ struct Rows {
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
       const float f = row_factor(most);
-      unit[i] = a.scale2 * row_unfactor(most);
+      unit[i] = row_unit(a, most);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // each warpgroup: times the scales of K in two parts, or as it is.
     auto queries = [&](int phase) {
       const float most = s_most[phase][row], f = row_factor(most);
-      unit = a.scale2 * row_unfactor(most);
+      unit = row_unit(a, most);
 #pragma unroll 1
       for (int c = w * (D / 16); c < (w + 1) * (D / 16); ++c) {
         uint32_t hi[4], lo[4];
