@@ -689,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 y = float_pair<BF16>(word(x, j));
-          split2(y.x * f * (phase ? 1.f : z[2 * j]), y.y * f * (phase ? 1.f : z[2 * j + 1]), hi[j], lo[j]);
+          // the scale first: with it the factor cannot overflow
+          split2(y.x * (phase ? 1.f : z[2 * j]) * f, y.y * (phase ? 1.f : z[2 * j + 1]) * f, hi[j], lo[j]);
         }
         tmem_st4(tq + 4 * c, hi);
         if (phase == 0) tmem_st4(tq + D / 2 + 4 * c, lo);

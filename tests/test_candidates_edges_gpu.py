@@ -36,3 +36,22 @@ def test_rows_and_scales_next_to_zero(T, dtype, mode):
     q[:] = 0
     for scale in (2.0 ** -149, 1.0, 2.0 ** 100, 3.4e38):
         check(cache, 0, q, k, v, parents, None, scale)
+
+
+@every_mode
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T", [2, 30])
+def test_scales_of_zero(T, dtype, mode):
+    # an imported state may have them where all codes are zero
+    g = gen(5)
+    cache = make_cache([90], 4, 2, 64, 16)
+    cache.set_tree_mode(mode)
+    u = cache.export_unit(0, 0)
+    u["k8"][:, 0], u["sK"][0], u["v8"][:, 0, 7], u["sV"][0, 7] = 0, 0.0, 0, 0.0
+    u["k8"][:, 1, 3], u["sK"][1, 3] = 0, 0.0
+    cache.import_unit(0, 0, u)
+    q, k, v = drafts(g, 1, T, 4, 2, 64, dtype)
+    check(cache, 0, 8 * q, k, v, tree("kary", 1, T, g))
+    q[0, 0, 2:] *= 2.0 ** -12                                                # beside one that counts
+    q[0, 0, 2:, 3] = 1000
+    check(cache, 0, q, k, v, tree("kary", 1, T, g))
