@@ -23,12 +23,22 @@ using namespace tc;
 constexpr int kMaxDrafts = 128;          // per sequence
 constexpr int kMaxSplit = 8;             // CTAs of a cluster that share the keys of some rows
 
-// Weights are fp16: exp2(score - reference + kLift).  The reference moves when
-// a score passes it by more than kLag bits, so a weight stays below 2^15.  Fp16
-// ends at 2^-24: a weight is off by at most 2^-25 - kLift of the reference's,
-// 2^-29.  The reference moves the less often the further it may lag, and a move
-// rescales the accumulator: with a lift of 11 and a lag of 4, and one key in
-// 200 three times as long, every other tile of 64 keys did.
+// Weights are exp2(score - reference + kLift), in fp16.  The kernel of few rows
+// holds them in two parts, off by 2^-22, which costs it 2 to 5 %.  The kernel of
+// many rows rounds them to one part, off by 2^-11 of each: half a step of an fp16
+// output, an eighth of that of a bf16 one, and less in a sum of many, whose
+// errors differ in sign.  Against the 64-bit values 0 to 61 drafts on 37 to 4097
+// entries in fp16 are off by 2.7e-4, rounded only at the end by 2.1e-4.
+// A second part there would be one more product, and as much again to split and
+// store: 64 drafts on four sequences of 8192 105 -> 119 us, 16 on eight of 2049
+// 32 -> 35, measured without the 32 KB of shared memory that it would need too.
+//
+// The reference moves when a score passes it by more than kLag bits, so a
+// weight stays below 2^15.  Fp16 ends at 2^-24: a weight is off by at most
+// 2^-25 - kLift of the reference's, 2^-29.  The reference moves the less often
+// the further it may lag, and a move rescales the accumulator: with a lift of 11
+// and a lag of 4, and one key in 200 three times as long, every other tile of 64
+// keys did.
 constexpr float kLift = 4.f, kLag = 11.f, kUnlift = 1.f / 16.f;
 
 struct Call {

@@ -8,9 +8,11 @@
 // a running reference, sum and output of all rows; the warps of a CTA, then the
 // CTAs of the cluster, add up their parts.
 //
-// Queries of INT8 keys are two fp16 parts.  Up to eight rows take one product
-// for both, the second part in rows 8 to 15, and the registers that saves hold
-// a second block in flight.
+// Queries of INT8 keys and all weights are two fp16 parts.  Up to eight rows
+// take one product for both, the second part in rows 8 to 15, and the registers
+// that saves hold a second block in flight.  The weights' second part took
+// eight single tokens of five heads on 2049 entries from 18.6 to 18.9 us (cache
+// not in L2); two drafts each, with a product of their own for it, 19.3 to 19.9.
 //
 // What bounds it: the latency of a warp's loads.  Eight single tokens on 2049
 // entries, 40 heads on 8: 14 us on the device for 38 MB (0.4 of the copy rate,
@@ -125,8 +127,9 @@ struct Rows {
       }
   }
 
-  // Weights of 16 keys from their scores.
-  __device__ __forceinline__ void weights(float (&x)[2][4], uint32_t (&p)[4]) {
+  // Weights of 16 keys from their scores, in two fp16 parts: PAIR as an
+  // operand, like the queries, which costs no product; else as two.
+  __device__ __forceinline__ void weights(float (&x)[2][4], uint32_t (&p)[4], uint32_t (&p2)[4]) {
     float top[kOf];
     bool move = false;
 #pragma unroll
@@ -152,7 +155,6 @@ struct Rows {
         o[j][3] *= f[kOf - 1];
       }
     }
-    p[1] = p[3] = 0u;
 #pragma unroll
     for (int i = 0; i < kOf; ++i) {
       const float base = ref[i] == -INFINITY ? 0.f : kLift - ref[i];
@@ -162,8 +164,13 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < 2; ++j) e[nt][j] = ex2(x[nt][2 * i + j] + base);
       l[i] += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
-      p[i] = pack2<false>(e[0][0], e[0][1]);
-      p[2 + i] = pack2<false>(e[1][0], e[1][1]);
+      if (PAIR) {
+        split2(e[0][0], e[0][1], p[0], p[1]);
+        split2(e[1][0], e[1][1], p[2], p[3]);
+      } else {
+        split2(e[0][0], e[0][1], p[i], p2[i]);
+        split2(e[1][0], e[1][1], p[2 + i], p2[2 + i]);
+      }
     }
   }
 };
@@ -247,13 +254,14 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
         for (int r = 0; r < NC; ++r) vc[r] = vn[at][r];
         if (i + kAhead * workers < nb8) fetch(i + kAhead * workers, at);
-        uint32_t p[4];
-        w.weights(x, p);
+        uint32_t p[4], p2[4];
+        w.weights(x, p, p2);
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
           uint32_t b0, b1;
           codes(word(vc[j >> 2], j & 3), b0, b1);
           mma(w.o[j], p, b0, b1);
+          if (!PAIR) mma(w.o[j], p2, b0, b1);
         }
       }
     }
@@ -342,12 +350,34 @@ __global__ void __launch_bounds__(kWarps * 32)
             b1 = word(y, 2 * (kk & 1) + 1);
           },
           [&](int e, int j) { return !(see[e] >> (8 * nt + 2 * t + j) & 1); });
-    uint32_t p[4];
-    w.weights(x, p);
+    uint32_t p[4], p2[4];
+    w.weights(x, p, p2);
+    // An infinite value times a second part, which may be zero or negative, would
+    // be NaN; x * 0 finds those that are not finite.
+    const __half2 zero = __float2half2_rn(0.f);
+    __half2 not_finite = zero;
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      const uint4& y = vc[j >> 1];
-      mma(w.o[j], p, word(y, 2 * (j & 1)), word(y, 2 * (j & 1) + 1));
+    for (int r = 0; r < 2 * NC; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t y = word(vc[r], j);
+        not_finite = __hfma2(*reinterpret_cast<const __half2*>(&y), zero, not_finite);
+      }
+    if (!__any_sync(0xffffffffu, !__hbeq2(not_finite, zero))) {
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        const uint4& y = vc[j >> 1];
+        mma(w.o[j], p, word(y, 2 * (j & 1)), word(y, 2 * (j & 1) + 1));
+        if (!PAIR) mma(w.o[j], p2, word(y, 2 * (j & 1)), word(y, 2 * (j & 1) + 1));
+      }
+    } else {                                             // the first part alone
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        const uint4& y = vc[j >> 1];
+        const float second[2] = {w.o[j][2], w.o[j][3]};
+        mma(w.o[j], p, word(y, 2 * (j & 1)), word(y, 2 * (j & 1) + 1));
+        if (PAIR) w.o[j][2] = second[0], w.o[j][3] = second[1];
+      }
     }
   }
 
@@ -359,7 +389,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (t == 0) s_stat[warp][g + 8 * i] = make_float2(w.ref[i], w.l[i]);
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
-      *reinterpret_cast<float2*>(&s_part[warp][g + 8 * i][8 * j + 2 * t]) = make_float2(w.o[j][2 * i], w.o[j][2 * i + 1]);
+      *reinterpret_cast<float2*>(&s_part[warp][g + 8 * i][8 * j + 2 * t]) =
+          PAIR ? make_float2(w.o[j][0] + w.o[j][2], w.o[j][1] + w.o[j][3]) : make_float2(w.o[j][2 * i], w.o[j][2 * i + 1]);
   }
   __syncthreads();
   constexpr int kCols = D / 4;

@@ -614,9 +614,10 @@ int confkv_selftest_prompt_timeout(const confkv_prompt_args* args, void* stream)
  *   are not read.
  * T is at most CONFKV_TREE_MAX_DRAFTS.  Scores, maxima, sums and the
  * accumulated output are fp32, the scales of INT8 keys are applied to q in two
- * fp16 parts; the weights are rounded to fp16 (below 2^-18 of the row's largest
- * off by up to 2^-29 of it instead of 2^-11 of themselves), the output once at
- * the end.
+ * fp16 parts, the output is rounded once at the end.  The weights are two fp16
+ * parts where few rows are taken (always for T Hq / Hkv <= 8 in the default
+ * mode): off by 2^-22 of themselves.  Many rows have them in one: off by 2^-11.
+ * In both cases by up to 2^-29 of the row's largest where that is more.
  * Non-finite values of drafts reach only the rows that see them.
  *   workspace: confkv_tree_workspace_bytes(ctx, T) of device memory (0 where the
  *   mode or the sizes rule out dealt keys: T Hq / Hkv <= 8 in the default mode,

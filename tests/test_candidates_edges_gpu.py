@@ -1,11 +1,12 @@
 """Calls of tree attention and beam selection at the ends of their ranges, and
 tree attention as it chooses its kernel by itself."""
+import math
 
 import pytest
 import torch
 
 from confidence_gated_kv_gb300 import binding
-from _candidates import BF16, F16, gen, make_cache
+from _candidates import BF16, F16, gen, make_cache, randn
 from test_tree_attention_gpu import check, drafts, tree
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +56,56 @@ def test_scales_of_zero(T, dtype, mode):
     q[0, 0, 2:] *= 2.0 ** -12                                                # beside one that counts
     q[0, 0, 2:, 3] = 1000
     check(cache, 0, q, k, v, tree("kary", 1, T, g))
+
+
+# ------------------------------------------------------- weights of few rows
+
+@pytest.mark.parametrize("Hq,T,mode", [(Hq, T, mode) for Hq, T in [(2, 1), (8, 1), (16, 1), (2, 3), (4, 4)] for mode in MODES[:2]]
+                         + [(2, 9, binding.TREE_ROWS), (16, 2, binding.TREE_ROWS), (6, 11, binding.TREE_ROWS)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_few_rows(d, Hq, T, mode):
+    """The kernel of few rows, which up to eight rows take by default.  Rows that see two entries of equal values but unlike sign, with weights
+    next to each other (and a draft of zeros): what is left is the weights' error.
+
+    Held in two fp16 parts a weight is off by 2^-22 of itself, its exponential
+    by 2^-21 and its score (below 0.01) by 2^-18 of 0.01; the products and the
+    join are five fp32 operations on it.  In all less than 2^-19 of the sum of
+    the magnitudes (below 1); one fp16 part alone is off by up to 2^-12."""
+    B, Hkv = 40, 2
+    g = gen(Hq + T)
+    cache = make_cache([2] * B, Hq, Hkv, d, 16, seed=3)
+    cache.set_tree_mode(mode)
+    keys = 0.002 * torch.randn((B, Hkv, d), generator=g).half()
+    for b in range(B):
+        u = cache.export_unit(b, 0)
+        u["k16"][0], u["k16"][1], u["v16"][0], u["v16"][1] = 0, keys[b].numpy(), 1, -1
+        cache.import_unit(b, 0, u)
+    q, k, v = drafts(g, B, T, Hq, Hkv, d, F16)
+    k[:], v[:] = 0, 0
+    out = cache.tree_attention(0, q, k, v, torch.full((T,), -1, dtype=torch.int32, device="cuda")).double().cpu()
+    score = torch.einsum("bthgd,bhd->bthg", q.view(B, T, Hkv, Hq // Hkv, d).double().cpu(), keys.double()) * d ** -0.5
+    assert 0.002 < float(score.abs().max()) < 0.012
+    want = (-score.expm1() / (2 + score.exp())).reshape(B, T, Hq, 1)
+    assert float(((out - want).abs() - 2.0 ** -11 * want.abs()).max()) <= 2.0 ** -19
+
+
+@every_mode
+@pytest.mark.parametrize("T", [1, 4, 7, 30])
+def test_infinite_values_of_the_cache(T, mode):
+    # as a step would leave them from values beyond fp16: they reach every row, in their channels
+    g = gen(T)
+    cache = make_cache([50], 4, 2, 64, 40)
+    cache.set_tree_mode(mode)
+    q, k, v = drafts(g, 1, T, 4, 2, 64, F16)
+    clean, _ = check(cache, 0, 0.1 * q, k, v)
+    u = cache.export_unit(0, 0)
+    u["v16"][3, 0, 5], u["v16"][7, 0, 9], u["v16"][9, 1, 63], u["v16"][0, 1, 8] = math.inf, -math.inf, math.inf, math.nan
+    cache.import_unit(0, 0, u)
+    out = cache.tree_attention(0, 0.1 * q, k, v)[0]
+    want = clean[0].clone()
+    want[:, :2, 5], want[:, :2, 9], want[:, 2:, 63], want[:, 2:, 8] = math.inf, -math.inf, math.inf, math.nan
+    assert torch.equal(out.isnan(), want.isnan())
+    ends = want.isinf() | want.isnan()
+    assert torch.equal(out[want.isinf()], want[want.isinf()])
+    # a block of such values takes its weights in one part
+    assert bool(((out - want).abs() <= 2.0 ** -10 * want.abs() + 2.0 ** -10)[~ends].all())
