@@ -12,7 +12,7 @@
 // a few more; these are ranked by counting.  Where more than kList reach it
 // (plateaus of equal values) the places are filled one at a time.
 //
-// Scores are sums of three fp32 numbers or pairs of them, kept as pairs
+// Scores are sums of four fp32 numbers or pairs of them, kept as pairs
 // (48 bits): fp64 arithmetic runs at 1/64 of the fp32 rate here, and its
 // comparisons alone would take the second kernel 10 us.
 //
@@ -266,17 +266,20 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
   return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
 }
 
-// score + logit - (hi + lo): a normalised pair as one number to compare.
+// score + (logit - most) - log sum: a normalised pair as one number to compare.
+// The beam's largest logit comes off first: as one number with the logarithm it
+// could be so large (all logits the type's lowest value) that nothing of that
+// is left.
 constexpr unsigned long long kNone = 0x007fffff00000000ull;      // of -inf
-__device__ __forceinline__ unsigned long long key_of(float score, float logit, float2 lse) {
-  const float2 a = two_sum(score, logit), b = two_sum(a.x, -lse.x);
-  const float2 r = two_sum(b.x, __fadd_rn(b.y, __fsub_rn(a.y, lse.y)));
+__device__ __forceinline__ unsigned long long key_of(float score, float logit, float most, float2 log_sum) {
+  const float2 a = two_sum(logit, -most), b = two_sum(a.x, score), c = two_sum(b.x, -log_sum.x);
+  const float2 r = two_sum(c.x, __fadd_rn(c.y, __fadd_rn(b.y, __fsub_rn(a.y, log_sum.y))));
   if (!(fabsf(r.x) < INFINITY)) return kNone;            // the sum leaves fp32
   return (unsigned long long)ordered(r.x) << 32 | ordered(r.y);
 }
 
 __global__ void __launch_bounds__(kJoin, 1) beam_join_kernel(const __grid_constant__ BeamArgs a) {
-  __shared__ float2 s_lse[kMaxN];
+  __shared__ float2 s_log[kMaxN];                        // of the sum of exponentials
   __shared__ float s_score[kMaxN], s_max[kMaxN], s_total[kMaxN];
   __shared__ float s_most[kJoin / 32][32];
   __shared__ unsigned long long s_key[kList];
@@ -330,12 +333,12 @@ __global__ void __launch_bounds__(kJoin, 1) beam_join_kernel(const __grid_consta
   // fp32 at 12 would be 5e-7.
   if (threadIdx.x < a.beams) {
     const int k = threadIdx.x;
-    const float score = a.scores[row0 + k], M = s_max[k];
-    const double lse = (double)M + log((double)s_total[k]);
-    const float hi = (float)lse;
-    if (!isfinite(score) || !isfinite(hi)) s_kind[k] = 0;
+    const float score = a.scores[row0 + k];
+    const double log_sum = log((double)s_total[k]);
+    const float hi = (float)log_sum;
+    if (!isfinite(score) || !isfinite(s_max[k]) || !isfinite(hi)) s_kind[k] = 0;
     s_score[k] = score;
-    s_lse[k] = make_float2(hi, (float)(lse - (double)hi));
+    s_log[k] = make_float2(hi, (float)(log_sum - (double)hi));
   }
   __syncthreads();
   // entry e of list i (a chunk of a beam), whose candidate is c
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kJoin, 1) beam_join_kernel(const __grid_consta
     }
     if (!(c.logit > -INFINITY)) return kNone;
     *at = (long long)k * a.V + c.token;
-    return key_of(s_score[k], c.logit, s_lse[k]);
+    return key_of(s_score[k], c.logit, s_max[k], s_log[k]);
   };
   auto load = [&](int i, int e) {
     return e == 0 && i < kJoin ? first : e == 0 && i < 2 * kJoin ? second : best[(long long)i * a.n + e];

@@ -5,11 +5,13 @@ import math
 import pytest
 import torch
 
+import confidence_gated_kv_gb300 as ck
 from confidence_gated_kv_gb300 import binding
 from _candidates import BF16, F16, gen, make_cache, randn
 from test_tree_attention_gpu import check, drafts, tree
 
 pytestmark = pytest.mark.gpu
+F32 = torch.float32
 MODES = [binding.TREE_AUTO, binding.TREE_ROWS, binding.TREE_TILES, binding.TREE_DEALT]
 NAMES = ["auto", "rows", "tiles", "dealt"]
 every_mode = pytest.mark.parametrize("mode", MODES, ids=NAMES)
@@ -109,3 +111,24 @@ def test_infinite_values_of_the_cache(T, mode):
     assert torch.equal(out[want.isinf()], want[want.isinf()])
     # a block of such values takes its weights in one part
     assert bool(((out - want).abs() <= 2.0 ** -10 * want.abs() + 2.0 ** -10)[~ends].all())
+
+
+# ------------------------------------------------------------------- beams
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("V", [5, 3001, 9000])
+def test_beams_whose_logits_are_all_the_lowest(V, dtype):
+    # as a mask leaves them that rules everything out: all tokens are equally likely
+    low = torch.finfo(dtype).min
+    x = torch.full((2, 2, V), low, dtype=dtype, device="cuda")
+    x[0, 1, 3] = 2.0                                                         # certain
+    x[1, 1] = -low / 2
+    got = ck.beam_select(x, torch.tensor([[-1.0, -2.0], [-3.0, -3.0]]).cuda(), 3)
+    each = -math.log(V)
+    want = [[(-2.0, 1, 3), (-1.0 + each, 0, 0), (-1.0 + each, 0, 1)], [(-3.0 + each, 0, i) for i in range(3)]]
+    if V == 5:
+        want[0] = sorted(want[0], reverse=True)
+    for i in range(2):
+        order = sorted(want[i], key=lambda w: (-w[0], w[1], w[2]))
+        assert got[1][i].tolist() == [w[1] for w in order] and got[2][i].tolist() == [w[2] for w in order]
+        assert all(abs(a - w[0]) <= 2.0 ** -18 + 2.0 ** -24 * abs(w[0]) for a, w in zip(got[0][i].tolist(), order))
