@@ -8,6 +8,7 @@ import torch
 import confidence_gated_kv_gb300 as ck
 from confidence_gated_kv_gb300 import binding
 from _candidates import BF16, F16, gen, make_cache, randn
+from test_beam_gpu import check as check_beams
 from test_tree_attention_gpu import check, drafts, tree
 
 pytestmark = pytest.mark.gpu
@@ -132,3 +133,12 @@ def test_beams_whose_logits_are_all_the_lowest(V, dtype):
         order = sorted(want[i], key=lambda w: (-w[0], w[1], w[2]))
         assert got[1][i].tolist() == [w[1] for w in order] and got[2][i].tolist() == [w[2] for w in order]
         assert all(abs(a - w[0]) <= 2.0 ** -18 + 2.0 ** -24 * abs(w[0]) for a, w in zip(got[0][i].tolist(), order))
+
+
+@pytest.mark.parametrize("beams,V,n", [(16, 5000, 32), (32, 5000, 64), (4, 20000, 17), (64, 700, 64)])
+@pytest.mark.parametrize("score", [-1000.0, -3000.0])
+def test_long_running_scores(beams, V, n, score):
+    g = gen(n)
+    x = randn(g, (2, beams, V)) * 3
+    check_beams(x, score + randn(g, (2, beams)), n)
+    check_beams(x + score, score + randn(g, (2, beams)), n)                  # and logits far from zero
