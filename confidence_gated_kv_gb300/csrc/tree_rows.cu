@@ -103,7 +103,9 @@ struct Rows {
   }
 
   // Scores of eight keys whose operands are b(kk, b0, b1), in log2 units; hide
-  // takes (row, column) of the lane's.
+  // takes (row, column) of the lane's.  EXACT: fp16 keys, for which the query's
+  // first part is exact and its second is left out (zero times an infinite key
+  // would be NaN where the score is -inf).
   template <bool EXACT, typename B, typename Hide>
   __device__ __forceinline__ void scores(float (&x)[4], B operands, Hide hidden) {
     float c[2][4] = {};
@@ -122,7 +124,7 @@ struct Rows {
     for (int i = 0; i < kOf; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float y = PAIR ? (c[0][j] + c[1][j]) + (c[0][2 + j] + c[1][2 + j]) : c[0][2 * i + j] + c[1][2 * i + j];
+        const float y = PAIR && !EXACT ? (c[0][j] + c[1][j]) + (c[0][2 + j] + c[1][2 + j]) : c[0][2 * i + j] + c[1][2 * i + j];
         x[2 * i + j] = hidden(i, j) ? -INFINITY : y * unit[i];
       }
   }

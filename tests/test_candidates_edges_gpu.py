@@ -114,6 +114,36 @@ def test_infinite_values_of_the_cache(T, mode):
     assert bool(((out - want).abs() <= 2.0 ** -10 * want.abs() + 2.0 ** -10)[~ends].all())
 
 
+@every_mode
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,Hq,T", [(64, 2, 1), (128, 8, 1), (64, 4, 4), (128, 4, 3), (64, 6, 5), (64, 4, 30)])
+def test_keys_that_are_infinitely_far(d, Hq, T, dtype, mode):
+    # a score of -inf (a key beyond fp16, in the cache or a draft) has no weight: as if the key were not there
+    g = gen(T)
+    cache = make_cache([30], Hq, 2, d, 40)
+    cache.set_tree_mode(mode)
+    u = cache.export_unit(0, 0)
+    q, k, v = drafts(g, 1, T + 1, Hq, 2, d, dtype)
+    q[..., 17] = q[..., 17].abs() + 0.5
+    roots = torch.full((T + 1,), -1, dtype=torch.int32, device="cuda")
+    below = torch.tensor([-1] + [0] * T, dtype=torch.int32, device="cuda")   # the others see draft 0
+    few = {name: u[name][[i for i in range(30) if i != 4]] for name in ("posR", "emaR", "k16", "v16")}
+    cache.import_unit(0, 0, {**u, **few})
+    if T == 1 and Hq == 8:                                                   # one token alone, as a single draft
+        q, k, v, roots, below = q[:, :1], k[:, :1], v[:, :1], roots[:1], roots[:1]
+    want, wlse = check(cache, 0, q, k, v, roots)
+    u["k16"][4, :, 17] = -math.inf
+    cache.import_unit(0, 0, u)
+    out, lse = cache.tree_attention(0, q, k, v, roots, return_lse=True)
+    step = torch.finfo(dtype).eps
+    near = lambda a, b: bool(((a - b).abs() <= 2 * step * b.abs() + 2.0 ** -11).all())  # noqa: E731
+    assert near(out.double(), want.double()) and near(lse, wlse)
+    if q.shape[1] > 1:
+        k[0, 0, :, 17] = -1e38 if dtype == BF16 else -math.inf
+        out, lse = cache.tree_attention(0, q, k, v, below, return_lse=True)
+        assert near(out[:, 1:].double(), want[:, 1:].double()) and near(lse[:, 1:], wlse[:, 1:])
+
+
 # ------------------------------------------------------------------- beams
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
