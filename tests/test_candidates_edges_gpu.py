@@ -7,7 +7,7 @@ import torch
 
 import confidence_gated_kv_gb300 as ck
 from confidence_gated_kv_gb300 import binding
-from _candidates import BF16, F16, gen, make_cache, randn
+from _candidates import BF16, F16, gen, make_cache, randn, tree_values
 from test_beam_gpu import check as check_beams
 from test_tree_attention_gpu import check, drafts, tree
 
@@ -142,6 +142,67 @@ def test_keys_that_are_infinitely_far(d, Hq, T, dtype, mode):
         k[0, 0, :, 17] = -1e38 if dtype == BF16 else -math.inf
         out, lse = cache.tree_attention(0, q, k, v, below, return_lse=True)
         assert near(out[:, 1:].double(), want[:, 1:].double()) and near(lse[:, 1:], wlse[:, 1:])
+
+
+# ---------------------------------------- the kernel that a call takes by itself
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 10, 2), (64, 3, 3), (128, 8, 1), (64, 6, 2)])
+@pytest.mark.parametrize("T", [1, 2, 5, 9, 16, 27, 64, 128])
+def test_default_mode_sizes(d, Hq, Hkv, T, dtype):
+    g = gen(T)
+    cache = make_cache([700, 0, 97], Hq, Hkv, d, 32, seed=T)
+    check(cache, 0, *drafts(g, 3, T, Hq, Hkv, d, dtype), tree("random", 3, T, g),
+          torch.tensor([T, T // 2, T], dtype=torch.int32).cuda())
+
+
+@pytest.mark.parametrize("lens", [[0], [1], [64], [129], [3000], [0, 2500, 17], [800] * 9, [9, 0, 1500, 40] * 4])
+@pytest.mark.parametrize("T", [1, 3, 12, 50])
+def test_default_mode_lengths(lens, T):
+    g = gen(len(lens))
+    cache = make_cache(lens, 10, 2, 128, 100, seed=T)
+    check(cache, 0, *drafts(g, len(lens), T, 10, 2, 128, BF16), tree("kary", len(lens), T, g))
+
+
+def test_default_mode_as_the_cache_grows():
+    # the host's bounds follow the steps, a captured call keeps the choice it was captured with, an import lifts them
+    g = gen(6)
+    cache = make_cache([40, 5], 10, 2, 64, 16, cap=4096)
+    T = 12
+    x = drafts(g, 2, T, 10, 2, 64, F16)
+    lens = torch.tensor([T, T], dtype=torch.int32).cuda()
+    out, _ = check(cache, 0, *x, None, lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.tree_attention(0, *x, None, lens, out=out)
+    for _ in range(3):
+        for _ in range(20):
+            cache.step(randn(g, (1, 2, 10, 64), F16), randn(g, (1, 2, 2, 64), F16), randn(g, (1, 2, 2, 64), F16), randn(g, (2, 300)))
+        check(cache, 0, *x, None, lens)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, _, tol, _ = tree_values(cache, 0, *x, None, lens, 64 ** -0.5)
+        assert bool(((out.double().cpu() - want).abs() <= tol).all())
+    long = make_cache([4000, 3000], 10, 2, 64, 16, cap=4096, seed=8)
+    for b in range(2):
+        cache.import_unit(b, 0, long.export_unit(b, 0))
+    check(cache, 0, *x, None, lens)
+    graph.replay()
+    torch.cuda.synchronize()
+    want, _, tol, _ = tree_values(cache, 0, *x, None, lens, 64 ** -0.5)
+    assert bool(((out.double().cpu() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("mode", [binding.TREE_AUTO, binding.TREE_DEALT], ids=["auto", "dealt"])
+@pytest.mark.parametrize("B,Hkv,G,T", [(153, 2, 2, 6), (310, 1, 1, 9), (10, 8, 8, 64)])
+def test_more_tiles_than_are_dealt(B, Hkv, G, T, mode):
+    g = gen(B)
+    lens = torch.randint(0, 300, (B,), generator=g).tolist()
+    cache = make_cache(lens, Hkv * G, Hkv, 64, 32)
+    cache.set_tree_mode(mode)
+    assert B * Hkv * -(-T * G // 128) > 304 and cache._tree_workspace_bytes(T) == 0
+    used = torch.randint(0, T + 1, (B,), generator=g).int().cuda()
+    check(cache, 0, *drafts(g, B, T, Hkv * G, Hkv, 64, F16), tree("random", B, T, g), used)
 
 
 # ------------------------------------------------------------------- beams
