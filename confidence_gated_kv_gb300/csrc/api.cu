@@ -481,7 +481,6 @@ static int tree_attention(confkv_ctx* ctx, const confkv_tree_args* p, bool test,
   tree::Call a{};
   a.layer = p->layer;
   a.T = p->T;
-  a.scale = p->scale;
   a.scale2 = p->scale * 1.4426950408889634f;
   a.q = static_cast<const uint16_t*>(p->q);
   a.k = static_cast<const uint16_t*>(p->k);

@@ -32,9 +32,12 @@
 #include "../../include/confkv.h"
 #include "confkv_internal.cuh"
 #include "fp32_pair.cuh"
+#include "tcgen05.cuh"
 
 namespace confkv {
 namespace {
+
+using tc::ex2;
 
 constexpr int kThreads = 256, kPer = 16, kChunk = kThreads * kPer;   // logits per CTA
 constexpr int kJoin = 512;               // threads of the second kernel
@@ -69,12 +72,6 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 template <typename T>
 constexpr int low_zeros() {
   return std::is_same_v<T, float> ? 0 : std::is_same_v<T, __half> ? 13 : 16;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // A float's bits in the order of its values (no NaN; -0 as 0).
@@ -190,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) beam_chunk_kernel(const __grid_const
 #pragma unroll
   for (int i = 0; i <= kPer; i += 2) {
     const float2 e = ((Pair(v[i], v[i + 1]) + Pair(off, off)) * Pair(1.4426950408889634f, 1.4426950408889634f)).get();
-    sums[i / 2 & 1] = sums[i / 2 & 1] + Pair(exp2_approx(e.x), exp2_approx(e.y));
+    sums[i / 2 & 1] = sums[i / 2 & 1] + Pair(ex2(e.x), ex2(e.y));
   }
   const float2 both = (sums[0] + sums[1]).get();
   float sum = both.x + both.y;
@@ -207,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) beam_chunk_kernel(const __grid_const
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, s_sum[w].x);
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) all += s_sum[w].y * (s_sum[w].x == top ? 1.f : exp2_approx((s_sum[w].x - top) * 1.4426950408889634f));
+    for (int w = 0; w < kThreads / 32; ++w) all += s_sum[w].y * (s_sum[w].x == top ? 1.f : ex2((s_sum[w].x - top) * 1.4426950408889634f));
     a.sums[list] = make_float2(top, all);
   }
   __syncthreads();
@@ -331,7 +328,7 @@ __global__ void __launch_bounds__(kJoin, 1) beam_join_kernel(const __grid_consta
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       // a chunk without a value above -inf adds its sum: zero, or NaN
       auto scaled = [&](float2 z) {
-        return z.x == M || z.x == -INFINITY ? z.y : z.y * exp2_approx((z.x - M) * 1.4426950408889634f);
+        return z.x == M || z.x == -INFINITY ? z.y : z.y * ex2((z.x - M) * 1.4426950408889634f);
       };
       sum = scaled(z0) + scaled(z1);
       for (int c = lane + 64; c < a.chunks; c += 32) sum += scaled(sums[c]);

@@ -46,7 +46,6 @@ struct Call {
   int split;                             // CTAs of a cluster that share the keys
   int tiles;                             // row tiles per (sequence, KV head)
   float scale2;                          // scale * log2(e)
-  float scale;
   const uint16_t *q, *k, *v;             // fp16 or bf16
   uint16_t* out;
   float* lse;
@@ -64,6 +63,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "r"(bytes), "r"(bar)
       : "memory");
 }
+
+__device__ __forceinline__ uint4 lds(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t& word(uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // Two 16-bit inputs as fp16 (a bf16 value beyond it becomes infinite).
 template <bool BF16>

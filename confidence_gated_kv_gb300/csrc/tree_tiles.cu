@@ -67,15 +67,6 @@ struct Tile {
 __device__ __forceinline__ void sts(uint32_t addr, uint32_t x) {
   asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(addr), "r"(x) : "memory");
 }
-__device__ __forceinline__ uint4 lds(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t& word(uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // A lane's words of a stored block are those of 8 x 8 matrices (lane 4 g + t:
 // row g, columns 2 t and 2 t + 1), whose rows stmatrix writes 16 bytes at a
