@@ -475,23 +475,30 @@ int launch(const Shape& s, const Dev& d, const Call& a, cudaStream_t st) {
 
 }  // namespace
 
-// Time in microseconds by a model that fits what was measured to a tenth: the
-// start and the join, then rounds of the CTAs that fit (two per SM, four of 64
-// channels) times a warp's blocks, 0.7 us each (1.1 where twice the warps share
-// the SM).  8 units of 2049 entries, 5 rows: 10.3 us; 64 units, 15 rows 16, 60
-// rows 31 us.
+// Time in microseconds by a model: 1, and for each wave of the CTAs that fit (two
+// per SM, four of 64 channels) a start and a join and what a warp takes for its
+// blocks, the longer the more CTAs share the memory: with 128 channels 0.44 a
+// block on an idle GPU, 0.79 with a CTA on every SM and 0.99 with two.  Fitted to
+// 75 calls of 9 to 512 rows with equal lengths, to a tenth: 9 rows on 2889
+// entries 12 us measured (11), 16 rows of 64 units on 5266 27 (28), 64 of 48 on
+// 3956 37 (36).  Up to eight rows 0.45 to 0.70; they always take this kernel, and
+// only the split follows.
 double plan_tree_rows(const Shape& s, int T, long long n8_bound, int* split) {
-  const int mine = T * s.G <= 8 ? 8 : kRows;
+  const bool pair = T * s.G <= 8;
+  const int mine = pair ? 8 : kRows;
   const long long tiles = ((long long)T * s.G + mine - 1) / mine, units = (long long)s.B * s.Hkv * tiles;
   const long long blocks = (n8_bound + 15) / 16 + s.WR / 16 + (T + 15) / 16, slots = s.D == 128 ? 304 : 608;
   double least = 1e30;
   for (int k = 1; k <= kMaxSplit; k *= 2) {              // clusters of other sizes leave more SMs idle
     if (k > 1 && units * k > slots) break;
     // us for a block of every warp of a CTA, by the CTAs of an SM
-    const double of_sm = (double)(units * k) / 152;
-    const double each = s.D == 128 ? 0.45 + 0.25 * std::min(std::max(of_sm - 1, 0.0), 1.0) : std::max(0.42, 0.21 * std::min(4.0, std::ceil(of_sm)));
+    const double of_sm = (double)(units * k) / 152, first = std::min(of_sm, 1.0), second = std::min(std::max(of_sm - 1, 0.0), 1.0);
+    const double each = s.D != 128 ? std::max(0.42, 0.21 * std::min(4.0, std::ceil(of_sm)))
+                        : pair     ? 0.45 + 0.25 * second
+                                   : 0.44 + 0.35 * first + 0.2 * second;
+    const double wave = s.D == 128 && !pair ? 7.0 : 6.0;
     const long long waves = (units * k + slots - 1) / slots;
-    const double t = 1.0 + 6.0 * (double)waves + each * (double)(waves * ((blocks + kWarps * k - 1) / (kWarps * k))) + (k > 1 ? 0.5 : 0.0);
+    const double t = 1.0 + wave * (double)waves + each * (double)(waves * ((blocks + kWarps * k - 1) / (kWarps * k))) + (k > 1 ? 0.5 : 0.0);
     if (t < least) {
       least = t;
       *split = k;

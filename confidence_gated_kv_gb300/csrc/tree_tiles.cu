@@ -975,16 +975,15 @@ int launch(const Shape& s, const Dev& d, const Call& a, cudaStream_t st) {
 
 }  // namespace
 
-// Time in microseconds by a model of what was measured: the start, the switch to
-// fp16 keys and the join (21 us, 14 with 64 channels), then rounds of resident
-// clusters times a CTA's tiles, 0.75 us each.  Clusters of one kind fill the
-// SMs of a GPC only in part, those of 7 and 8 CTAs a good two thirds of the GPU.
-// us that an SM takes for `ctas` CTAs, one after the other, of `tiles` each; a
-// CTA after another starts on fetched instructions
+// Time in microseconds by a model: for the CTAs of an SM, one after the other, the
+// start, the switch to fp16 keys and the join (19, 13 with 64 channels; 0.7 of that
+// for each after the first, which finds its instructions fetched), and 0.76 a tile.
 static double tiles_time(const Shape& s, long long ctas, long long tiles) {
   return (s.D == 128 ? 19.0 : 13.0) * (0.3 + 0.7 * (double)ctas) + 0.76 * (double)(ctas * tiles);
 }
 
+// Rounds of the clusters that are resident: those of one kind fill the SMs of a GPC
+// only in part, those of 7 and 8 CTAs a good two thirds of the GPU.
 double plan_tree_tiles(const Shape& s, int T, long long n8_bound, int* split) {
   static const int resident[kMaxSplit + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
   const long long units = (long long)s.B * s.Hkv * (((long long)T * s.G + kRows - 1) / kRows);

@@ -623,7 +623,9 @@ int confkv_selftest_prompt_timeout(const confkv_prompt_args* args, void* stream)
  *   mode or the sizes rule out dealt keys: T Hq / Hkv <= 8 in the default mode,
  *   or more than 304 tiles of 128 rows), 16-byte aligned, for this call alone:
  *   nothing in it has to be set before or is kept after.  CONFKV_ECAPACITY for
- *   less than that.
+ *   less than that.  The default mode asks for it (some 20 MB with 128 channels)
+ *   also for calls that then take a kernel without dealt keys: which one depends
+ *   on the lengths at the call.
  * Needs a prefilled context (else CONFKV_ESTATE); asynchronous on `stream`;
  * may be captured, and a replay reads the cache as it then is.  Calls on
  * several streams may run at once as long as nothing writes the cache.  The
