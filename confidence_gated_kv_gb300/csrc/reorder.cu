@@ -11,7 +11,9 @@
 // What bounds it: HBM, reads and writes mixed.  With few parents a thread takes
 // several columns at once, so that eight loads are in flight.  Two groups of
 // eight beams with 8192 entries, four layers: 207 us for 1.06 GB (0.77 of the
-// copy rate).  Lengths by the last CTA of a group instead of a launch of their
+// copy rate).  More than eight beams wait in shared memory, one batch of copies at
+// a time: two groups of 16 with 2049 entries 168 to 258 us (0.71 to 0.66, by how
+// many move), one of 64 in two layers 422 to 764 (0.30 to 0.23).  Lengths by the last CTA of a group instead of a launch of their
 // own took 4 us more on the device and 4 less on the host.
 #include <cuda_runtime.h>
 #include <algorithm>

@@ -27,11 +27,12 @@ constexpr int kMaxSplit = 8;             // CTAs of a cluster that share the key
 // holds them in two parts, off by 2^-22, which costs it 2 to 5 %.  The kernel of
 // many rows rounds them to one part, off by 2^-11 of each: half a step of an fp16
 // output, an eighth of that of a bf16 one, and less in a sum of many, whose
-// errors differ in sign.  Against the 64-bit values 0 to 61 drafts on 37 to 4097
-// entries in fp16 are off by 2.7e-4, rounded only at the end by 2.1e-4.
-// A second part there would be one more product, and as much again to split and
-// store: 64 drafts on four sequences of 8192 105 -> 119 us, 16 on eight of 2049
-// 32 -> 35, measured without the 32 KB of shared memory that it would need too.
+// errors differ in sign.  A second part there was built and measured, fp16 inputs:
+// 0 to 61 drafts on 37 to 4097 entries, whose relative error against 64 bits is
+// 2.6e-4 with one part and 2.1e-4 where only the output is rounded, took 45 us
+// instead of 39, 64 drafts on four sequences of 8192 124 instead of 103, 16 on
+// eight of 2049 38 instead of 32, most of it to split and to store the weights.
+// With bf16 outputs the error is the output's rounding, 1.7e-3, either way.
 //
 // The reference moves when a score passes it by more than kLag bits, so a
 // weight stays below 2^15.  Fp16 ends at 2^-24: a weight is off by at most

@@ -15,8 +15,9 @@
 // not in L2); two drafts each, with a product of their own for it, 19.3 to 19.9.
 //
 // What bounds it: the latency of a warp's loads.  Eight single tokens on 2049
-// entries, 40 heads on 8: 14 us on the device for 38 MB (0.4 of the copy rate,
-// eight warps an SM).  Copies through shared memory, a ring per warp, took 19.
+// entries, 40 heads on 8, 38 MB: 15 us on the device, 19 with nothing of it in L2
+// (0.3 of the copy rate, eight warps an SM).  Copies through shared memory, a ring
+// per warp, took a third longer.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <algorithm>
